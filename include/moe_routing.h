@@ -381,6 +381,166 @@ MOE_API int moe_fill_shared_expert_slot_philox(float* topk_weights, int32_t* top
  */
 MOE_API int moe_sort_topk_by_id(float* topk_weights, int32_t* topk_ids, int64_t M, int32_t k, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The expert layer around the routing: tokens sorted by expert and brought
+ * back, the experts' products, and the gradients down to the router's logits.
+ * (Added to version 5; no earlier call changed.)  Further conventions:
+ *
+ *   - k slots a token, P = M * k pairs, pair index i = token * k + slot;
+ *     scatter_indx and expert_offsets are moe_expert_permutation's.  A pair
+ *     with scatter_indx < 0 has no place: nothing is copied for it, it adds
+ *     nothing to a sum, and its weight's gradient is 0.  (Entries >= P are
+ *     read the same way.)
+ *   - Rows at and behind expert_offsets[E] belong to no expert: those of an
+ *     output are left as they were, those of an input have no effect,
+ *     whatever they hold.  Offsets are read as if clamped to [0, P]; an
+ *     expert whose end is not above its start has no rows.
+ *   - Row types are MOE_DTYPE_F32 or MOE_DTYPE_BF16; sums are fp32, rounded
+ *     once when they are stored.  Results do not depend on timing: the same
+ *     inputs give the same bits.
+ *   - Outputs must not overlap inputs or one another.
+ *   - M * k (or P) must be below 2^31, else MOE_ERR_UNSUPPORTED.  M == 0 or
+ *     P == 0 is valid (moe_expert_matmul_grad_weight then writes zeros).
+ */
+
+typedef enum {
+    MOE_ACT_NONE = 0, /* f(z) = z                                            */
+    MOE_ACT_SILU = 1, /* f(z) = z / (1 + exp(-z))                            */
+    MOE_ACT_GELU = 2  /* f(z) = z * Phi(z), Phi the normal distribution      */
+} moe_activation_t;
+
+/*
+ * moe_gather_tokens - token rows to their places in expert order:
+ *     sorted[scatter_indx[t * k + j]] = x[t]
+ *   x             device, (M, H) of `dtype`
+ *   H             columns, H >= 1 (rows that 16-byte accesses can reach are
+ *                 moved fastest: H a multiple of 8 in bf16, of 4 in fp32)
+ *   scatter_indx  device, int32 (M * k)
+ *   sorted        device, (M * k, H) of `dtype` out
+ */
+MOE_API int moe_gather_tokens(const void* x, int dtype, int64_t M, int32_t H, const int32_t* scatter_indx,
+                              int32_t k, void* sorted, void* stream);
+
+/*
+ * moe_gather_tokens_backward - the gradient of moe_gather_tokens:
+ *     grad_x[t] = sum_j grad_sorted[scatter_indx[t * k + j]]   (j ascending)
+ *   grad_sorted   device, (M * k, H) of `dtype`
+ *   grad_x        device, (M, H) of `dtype` out
+ */
+MOE_API int moe_gather_tokens_backward(const void* grad_sorted, int dtype, int64_t M, int32_t H,
+                                       const int32_t* scatter_indx, int32_t k, void* grad_x, void* stream);
+
+/*
+ * moe_combine_tokens - the experts' rows back to their tokens, weighted:
+ *     out[t] = residual[t] + sum_j topk_weights[t, j] * y[scatter_indx[t * k + j]]
+ *   y             device, (M * k, H) of `dtype`, rows in expert order
+ *   topk_weights  device, fp32 (M, k)
+ *   residual      device, (M, H) of `dtype`, or NULL
+ *   out           device, (M, H) of `dtype` out
+ */
+MOE_API int moe_combine_tokens(const void* y, int dtype, int64_t M, int32_t H, const int32_t* scatter_indx,
+                               int32_t k, const float* topk_weights, const void* residual, void* out,
+                               void* stream);
+
+/*
+ * moe_combine_tokens_backward - the gradients of moe_combine_tokens with
+ * respect to y and topk_weights (the residual's is grad_out itself):
+ *     grad_y[scatter_indx[t * k + j]] = topk_weights[t, j] * grad_out[t]
+ *     grad_weights[t, j]              = <grad_out[t], y[scatter_indx[t * k + j]]>
+ *   grad_out      device, (M, H) of `dtype`
+ *   grad_y        device, (M * k, H) of `dtype` out
+ *   grad_weights  device, fp32 (M, k) out
+ */
+MOE_API int moe_combine_tokens_backward(const void* grad_out, const void* y, int dtype, int64_t M, int32_t H,
+                                        const int32_t* scatter_indx, int32_t k, const float* topk_weights,
+                                        void* grad_y, float* grad_weights, void* stream);
+
+/*
+ * moe_expert_matmul - each row of x times its expert's weight, with bias,
+ * activation and residual in the same pass; for the rows p of expert e
+ * (expert_offsets[e] <= p < expert_offsets[e + 1]):
+ *     z[p]   = weight[e] x[p] + bias[e]
+ *     out[p] = f(z[p]) + residual[p]                              (gated = 0)
+ *     out[p] = f(z[p][0:N]) * z[p][N:2N] + residual[p]            (gated = 1)
+ *   x              device, (P, K) bf16, 16-byte aligned
+ *   weight         device, (E, Nz, K) bf16, 16-byte aligned; Nz = N, or 2 N
+ *                  when gated (the gate's rows, then the other factor's)
+ *   expert_offsets device, int32 (E + 1).  A plain matrix product is E = 1
+ *                  with offsets {0, P}
+ *   K, N           positive multiples of 8 (else MOE_ERR_UNSUPPORTED)
+ *   E              experts, 1 <= E <= 1024
+ *   bias           device, fp32 (E, Nz), or NULL
+ *   activation     f: MOE_ACT_NONE, MOE_ACT_SILU or MOE_ACT_GELU
+ *   residual       device, (P, N) bf16, 16-byte aligned, or NULL
+ *   out            device, (P, N) bf16 out, 16-byte aligned
+ *   preact_out     device, (P, Nz) bf16 out, 16-byte aligned, or NULL: z, for
+ *                  the backward pass (the activation itself is taken of the
+ *                  fp32 z)
+ */
+MOE_API int moe_expert_matmul(const void* x, const void* weight, const int32_t* expert_offsets, int64_t P,
+                              int32_t K, int32_t N, int32_t E, const float* bias, int activation, int32_t gated,
+                              const void* residual, void* out, void* preact_out, void* stream);
+
+/*
+ * moe_expert_matmul_grad_input - the gradient with respect to x of
+ * moe_expert_matmul without activation, taken on through the activation that
+ * produced x:
+ *     q[p]      = weight[e]^T grad_out[p]
+ *     grad_x[p] = q[p]                                    preact NULL
+ *     grad_x[p] = q[p] * f'(z[p])                         preact (P, K), gated = 0
+ *     grad_x[p] = (q[p] * u * f'(g), q[p] * f(g))         preact (P, 2 K) = (g, u), gated = 1
+ *   grad_out   device, (P, N) bf16, 16-byte aligned
+ *   weight     device, (E, N, K) bf16, 16-byte aligned
+ *   preact     device, bf16, 16-byte aligned, or NULL (then activation must be
+ *              MOE_ACT_NONE and gated 0)
+ *   grad_x     device, (P, K) bf16 out, or (P, 2 K) when gated, 16-byte aligned
+ *   K, N, E    as moe_expert_matmul
+ */
+MOE_API int moe_expert_matmul_grad_input(const void* grad_out, const void* weight, const int32_t* expert_offsets,
+                                         int64_t P, int32_t K, int32_t N, int32_t E, const void* preact,
+                                         int activation, int32_t gated, void* grad_x, void* stream);
+
+/*
+ * moe_expert_matmul_grad_weight - the gradients with respect to weight and
+ * bias of moe_expert_matmul without activation:
+ *     grad_weight[e] = sum_{p of e} grad_out[p] x[p]^T,   grad_bias[e] = sum_{p of e} grad_out[p]
+ * (zeros for an expert without rows).
+ *   grad_out     device, (P, N) bf16, 16-byte aligned
+ *   x            device, (P, K) bf16, 16-byte aligned
+ *   grad_weight  device, (E, N, K) of `dtype` out, 16-byte aligned
+ *   grad_bias    device, fp32 (E, N) out, or NULL
+ *   K, N, E      as moe_expert_matmul
+ */
+MOE_API int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int32_t* expert_offsets,
+                                          int64_t P, int32_t K, int32_t N, int32_t E, int dtype, void* grad_weight,
+                                          float* grad_bias, void* stream);
+
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* moe_topk_softmax, moe_grouped_topk(_softcap)    */
+    MOE_SCORE_SIGMOID = 1  /* moe_biased_grouped_topk(_aiter), fused routers  */
+} moe_scoring_t;
+
+/*
+ * moe_topk_backward - the gradient of a routing call's weights with respect to
+ * its logits, the choice of experts held fixed (groups and correction bias
+ * only steer the choice, so they do not appear).  With p the scores (softmax
+ * of the row or sigmoid, of softcap * tanh(x / softcap) if softcap != 0):
+ *     w_j = routed_scaling_factor * p_{id_j} [/ sum_l p_{id_l} if renormalize]
+ *     grad_logits = sum_j grad_weights_j * dw_j / dx
+ *   grad_weights   device, fp32 (M, k)
+ *   gating_output  device, (M, E) of `dtype`: the logits that were routed
+ *   topk_ids       device, int32 (M, k): the routing call's ids.  Ids outside
+ *                  [0, E) (a shared-expert slot) are left out of every sum
+ *   scoring        MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
+ *   softcap        finite, 0 = none; only with MOE_SCORE_SOFTMAX
+ *   grad_logits    device, (M, E) of `dtype` out (written whole)
+ *   E <= 1024, 1 <= k <= 32, M * k below 2^31
+ */
+MOE_API int moe_topk_backward(const float* grad_weights, const void* gating_output, int dtype,
+                              const int32_t* topk_ids, int64_t M, int32_t E, int32_t k, int scoring,
+                              int32_t renormalize, float routed_scaling_factor, float softcap, void* grad_logits,
+                              void* stream);
+
 /*
  * moe_selftest_bounded_wait - checks the failure path of the library's
  * bounded waits without a fault: one thread waits on an mbarrier that nothing

@@ -4,6 +4,16 @@ The compute lives in ``libmoe_routing.so`` (hand-written CUDA kernels behind
 the C ABI in ``include/moe_routing.h``); this package is its thin binding.
 Build the library with ``python -m moe_expert_routing_token_b200.build``.
 """
+from .experts import (  # noqa: F401
+    combine_tokens,
+    combine_tokens_backward,
+    expert_matmul,
+    expert_matmul_grad_input,
+    expert_matmul_grad_weight,
+    gather_tokens,
+    gather_tokens_backward,
+    topk_backward,
+)
 from .routing import (  # noqa: F401
     MOE_DTYPE_BF16,
     MOE_DTYPE_F32,
@@ -29,4 +39,6 @@ __all__ = [
     "topk_softmax", "grouped_topk", "biased_grouped_topk", "fused_router_topk",
     "fused_router_workspace_size", "lib", "RoutingError", "watchdog_trips", "expert_permutation",
     "expert_permutation_workspace_size", "fill_shared_expert_slot", "fill_shared_expert_slot_philox", "sort_topk_by_id", "fused_router_top1",
+    "gather_tokens", "gather_tokens_backward", "combine_tokens", "combine_tokens_backward", "expert_matmul",
+    "expert_matmul_grad_input", "expert_matmul_grad_weight", "topk_backward",
 ]

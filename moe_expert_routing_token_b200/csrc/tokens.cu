@@ -1,0 +1,356 @@
+// Token rows to their places in expert order and back, with gradients:
+//
+//   moe_gather_tokens            sorted[s(t, j)] = x[t]
+//   moe_gather_tokens_backward   grad_x[t] = sum_j grad_sorted[s(t, j)]
+//   moe_combine_tokens           out[t] = residual[t] + sum_j w[t, j] y[s(t, j)]
+//   moe_combine_tokens_backward  grad_y[s(t, j)] = w[t, j] grad_out[t],
+//                                grad_w[t, j] = <grad_out[t], y[s(t, j)]>
+//
+// s is the expert permutation's scatter index (token-major), so every kernel
+// walks tokens: a token's own row is read or written once and its k places
+// are visited from registers.  No arithmetic to speak of; HBM traffic bounds
+// all four.  Sums run over j ascending in fp32, so results do not depend on
+// scheduling.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstdio>
+
+#include "moe_routing.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+int set_error(int status, const char* msg);
+int set_cuda_error(cudaError_t err, const char* what);
+
+namespace {
+
+constexpr int kTokThreads = 128;
+constexpr int kTokWarps = kTokThreads / 32;
+
+// VB bytes of a row as one access; N values of T in it.
+template <int VB> struct Vec;
+template <> struct Vec<16> { using type = uint4; };
+template <> struct Vec<8> { using type = uint2; };
+template <> struct Vec<4> { using type = uint32_t; };
+template <> struct Vec<2> { using type = uint16_t; };
+
+template <typename T, int VB>
+struct Chunk {
+    static constexpr int N = VB / (int)sizeof(T);
+    using V = typename Vec<VB>::type;
+    union {
+        V v;
+        T t[N];
+    };
+    __device__ __forceinline__ Chunk() {}
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// One warp per (token, segment of 32 * U accesses of the row).
+template <typename T, int VB, int U>
+__global__ void __launch_bounds__(kTokThreads)
+    gather_kernel(const T* x, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
+                  T* sorted, int segs) {
+    using C = Chunk<T, VB>;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
+    ptx::griddep_wait();
+    if (item >= M * segs) return;
+    const int64_t t = item / segs;
+    const int64_t c0 = (item % segs) * (32 * U) + lane;  // this lane's first access in the row
+    const int64_t n = H / C::N;
+    typename C::V v[U];
+    const auto* src = reinterpret_cast<const typename C::V*>(x + t * H);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < n) v[u] = src[c0 + 32 * u];
+    for (int j = 0; j < k; ++j) {
+        const uint32_t p = (uint32_t)__ldg(scatter + t * k + j);
+        if (p >= P) continue;
+        auto* dst = reinterpret_cast<typename C::V*>(sorted + (int64_t)p * H);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < n) dst[c0 + 32 * u] = v[u];
+    }
+}
+
+// One warp per (token, segment): the weighted sum of the token's rows.
+template <typename T, int VB, int U, bool WEIGHTED>
+__global__ void __launch_bounds__(kTokThreads)
+    combine_kernel(const T* y, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
+                   const float* __restrict__ weights, const T* residual, T* out, int segs) {
+    using C = Chunk<T, VB>;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
+    ptx::griddep_wait();
+    if (item >= M * segs) return;
+    const int64_t t = item / segs;
+    const int64_t c0 = (item % segs) * (32 * U) + lane;
+    const int64_t n = H / C::N;
+    float acc[U][C::N];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) acc[u][i] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const uint32_t p = (uint32_t)__ldg(scatter + t * k + j);
+        if (p >= P) continue;
+        const float w = WEIGHTED ? __ldg(weights + t * k + j) : 1.0f;
+        const auto* src = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c0 + 32 * u >= n) continue;
+            C c;
+            c.v = src[c0 + 32 * u];
+#pragma unroll
+            for (int i = 0; i < C::N; ++i)
+                acc[u][i] = WEIGHTED ? fmaf(w, to_f32(c.t[i]), acc[u][i]) : acc[u][i] + to_f32(c.t[i]);
+        }
+    }
+    const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H);
+    auto* dst = reinterpret_cast<typename C::V*>(out + t * H);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (c0 + 32 * u >= n) continue;
+        C c;
+        if (residual != nullptr) {
+            c.v = res[c0 + 32 * u];
+#pragma unroll
+            for (int i = 0; i < C::N; ++i) acc[u][i] += to_f32(c.t[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) c.t[i] = from_f32<T>(acc[u][i]);
+        dst[c0 + 32 * u] = c.v;
+    }
+}
+
+// One block per token; KB slots a pass, their dot products in registers and
+// then summed over the block in a fixed order.
+constexpr int KB = 8;
+template <typename T, int VB>
+__global__ void __launch_bounds__(kTokThreads)
+    combine_backward_kernel(const T* grad_out, const T* y, int64_t H, const int32_t* __restrict__ scatter, int k,
+                            uint32_t P, const float* __restrict__ weights, T* grad_y, float* grad_weights) {
+    using C = Chunk<T, VB>;
+    __shared__ float s_dot[kTokWarps][KB];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = H / C::N;
+    ptx::griddep_wait();
+    const auto* g_row = reinterpret_cast<const typename C::V*>(grad_out + t * H);
+    for (int j0 = 0; j0 < k; j0 += KB) {
+        uint32_t p[KB];
+        float w[KB], dot[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            p[j] = j0 + j < k ? (uint32_t)__ldg(scatter + t * k + j0 + j) : 0xffffffffu;
+            w[j] = p[j] < P ? __ldg(weights + t * k + j0 + j) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t c = threadIdx.x; c < n; c += kTokThreads) {
+            C g;
+            g.v = g_row[c];
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                if (p[j] >= P) continue;
+                C v, d;
+                v.v = reinterpret_cast<const typename C::V*>(y + (int64_t)p[j] * H)[c];
+#pragma unroll
+                for (int i = 0; i < C::N; ++i) {
+                    dot[j] = fmaf(to_f32(g.t[i]), to_f32(v.t[i]), dot[j]);
+                    d.t[i] = from_f32<T>(w[j] * to_f32(g.t[i]));
+                }
+                reinterpret_cast<typename C::V*>(grad_y + (int64_t)p[j] * H)[c] = d.v;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < KB; ++j) s_dot[warp][j] = dot[j];
+        __syncthreads();
+        if (threadIdx.x < KB && j0 + (int)threadIdx.x < k) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kTokWarps; ++i) s += s_dot[i][threadIdx.x];
+            grad_weights[t * k + j0 + threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
+bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Widest access that keeps every row of these arrays aligned.
+template <typename T>
+int access_bytes(int64_t H, const void* a, const void* b, const void* c = nullptr) {
+    const size_t row = (size_t)H * sizeof(T);
+    for (int vb = 16; vb > (int)sizeof(T); vb /= 2)
+        if (row % vb == 0 && al(a, vb) && al(b, vb) && (!c || al(c, vb))) return vb;
+    return sizeof(T);
+}
+
+template <typename... KArgs, typename... Args>
+int launch(void (*kern)(KArgs...), int64_t blocks, const char* who, void* stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(kTokThreads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+    return err == cudaSuccess ? MOE_OK : set_cuda_error(err, who);
+}
+
+struct TokArgs {
+    const char* who;
+    int64_t M, H;
+    const int32_t* scatter;
+    int k;
+    void* stream;
+};
+
+// Shared checks.  Returns MOE_OK to go on, -1 for an empty batch.
+int check(const TokArgs& a, int dtype, std::initializer_list<const void*> rows, std::initializer_list<const void*> words) {
+    char msg[256];
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) {
+        snprintf(msg, sizeof msg, "%s: dtype %d is neither MOE_DTYPE_F32 nor MOE_DTYPE_BF16", a.who, dtype);
+        return set_error(MOE_ERR_INVALID_ARG, msg);
+    }
+    if (a.M < 0 || a.H < 1 || a.k < 1) {
+        snprintf(msg, sizeof msg, "%s: M=%lld must not be negative, H=%lld and k=%d must be positive", a.who,
+                 (long long)a.M, (long long)a.H, a.k);
+        return set_error(MOE_ERR_INVALID_ARG, msg);
+    }
+    if (a.M > ((1ll << 31) - 1) / a.k) {
+        snprintf(msg, sizeof msg, "%s: M*k >= 2^31", a.who);
+        return set_error(MOE_ERR_UNSUPPORTED, msg);
+    }
+    if (a.M == 0) return -1;
+    const size_t esz = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    for (const void* p : rows)
+        if (!p || !al(p, esz)) {
+            snprintf(msg, sizeof msg, "%s: a row array is null or not aligned to its element size", a.who);
+            return set_error(MOE_ERR_INVALID_ARG, msg);
+        }
+    for (const void* p : words)
+        if (!p || !al(p, 4)) {
+            snprintf(msg, sizeof msg, "%s: an index or weight array is null or not 4-byte aligned", a.who);
+            return set_error(MOE_ERR_INVALID_ARG, msg);
+        }
+    return MOE_OK;
+}
+
+// Accesses in flight per lane and row segment.
+constexpr int kUnroll = 4;
+
+template <typename T, int VB>
+int run_gather(const TokArgs& a, const void* x, void* sorted) {
+    const int64_t n = a.H / (VB / (int)sizeof(T));
+    const int segs = (int)((n + 32 * kUnroll - 1) / (32 * kUnroll));
+    const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
+    if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_gather_tokens: M*H needs too many blocks");
+    return launch(gather_kernel<T, VB, kUnroll>, blocks, a.who, a.stream, (const T*)x, a.M, a.H, a.scatter, a.k,
+                  (uint32_t)(a.M * a.k), (T*)sorted, segs);
+}
+
+template <typename T, int VB, bool WEIGHTED>
+int run_combine(const TokArgs& a, const void* y, const float* w, const void* residual, void* out) {
+    constexpr int U = 2;
+    const int64_t n = a.H / (VB / (int)sizeof(T));
+    const int segs = (int)((n + 32 * U - 1) / (32 * U));
+    const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
+    if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_combine_tokens: M*H needs too many blocks");
+    return launch(combine_kernel<T, VB, U, WEIGHTED>, blocks, a.who, a.stream, (const T*)y, a.M, a.H, a.scatter, a.k,
+                  (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, segs);
+}
+
+template <typename T, int VB>
+int run_combine_backward(const TokArgs& a, const void* g, const void* y, const float* w, void* gy, float* gw) {
+    return launch(combine_backward_kernel<T, VB>, a.M, a.who, a.stream, (const T*)g, (const T*)y, a.H, a.scatter, a.k,
+                  (uint32_t)(a.M * a.k), w, (T*)gy, gw);
+}
+
+// F<T, VB>(args...) for the row type and access width.
+#define MOE_TOK_DISPATCH(F, dtype, vb32, vb16, ...)                        \
+    do {                                                                   \
+        if ((dtype) == MOE_DTYPE_F32) {                                    \
+            switch (vb32) {                                                \
+                case 16: return F(float, 16)(__VA_ARGS__);                 \
+                case 8: return F(float, 8)(__VA_ARGS__);                   \
+                default: return F(float, 4)(__VA_ARGS__);                  \
+            }                                                              \
+        }                                                                  \
+        switch (vb16) {                                                    \
+            case 16: return F(__nv_bfloat16, 16)(__VA_ARGS__);             \
+            case 8: return F(__nv_bfloat16, 8)(__VA_ARGS__);               \
+            case 4: return F(__nv_bfloat16, 4)(__VA_ARGS__);               \
+            default: return F(__nv_bfloat16, 2)(__VA_ARGS__);              \
+        }                                                                  \
+    } while (0)
+#define MOE_GATHER(T, VB) run_gather<T, VB>
+#define MOE_COMBINE(T, VB) run_combine<T, VB, true>
+#define MOE_SUM(T, VB) run_combine<T, VB, false>
+#define MOE_COMBINE_BWD(T, VB) run_combine_backward<T, VB>
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_gather_tokens(const void* x, int dtype, int64_t M, int32_t H, const int32_t* scatter_indx, int32_t k,
+                      void* sorted, void* stream) {
+    using namespace moe;
+    const TokArgs a{"moe_gather_tokens", M, H, scatter_indx, k, stream};
+    const int rc = check(a, dtype, {x, sorted}, {scatter_indx});
+    if (rc != MOE_OK) return rc < 0 ? MOE_OK : rc;
+    MOE_TOK_DISPATCH(MOE_GATHER, dtype, access_bytes<float>(H, x, sorted), access_bytes<__nv_bfloat16>(H, x, sorted),
+                     a, x, sorted);
+}
+
+int moe_gather_tokens_backward(const void* grad_sorted, int dtype, int64_t M, int32_t H,
+                               const int32_t* scatter_indx, int32_t k, void* grad_x, void* stream) {
+    using namespace moe;
+    const TokArgs a{"moe_gather_tokens_backward", M, H, scatter_indx, k, stream};
+    const int rc = check(a, dtype, {grad_sorted, grad_x}, {scatter_indx});
+    if (rc != MOE_OK) return rc < 0 ? MOE_OK : rc;
+    MOE_TOK_DISPATCH(MOE_SUM, dtype, access_bytes<float>(H, grad_sorted, grad_x),
+                     access_bytes<__nv_bfloat16>(H, grad_sorted, grad_x), a, grad_sorted, nullptr, nullptr, grad_x);
+}
+
+int moe_combine_tokens(const void* y, int dtype, int64_t M, int32_t H, const int32_t* scatter_indx, int32_t k,
+                       const float* topk_weights, const void* residual, void* out, void* stream) {
+    using namespace moe;
+    const TokArgs a{"moe_combine_tokens", M, H, scatter_indx, k, stream};
+    const int rc = check(a, dtype, {y, residual ? residual : y, out}, {scatter_indx, topk_weights});
+    if (rc != MOE_OK) return rc < 0 ? MOE_OK : rc;
+    MOE_TOK_DISPATCH(MOE_COMBINE, dtype, access_bytes<float>(H, y, out, residual),
+                     access_bytes<__nv_bfloat16>(H, y, out, residual), a, y, topk_weights, residual, out);
+}
+
+int moe_combine_tokens_backward(const void* grad_out, const void* y, int dtype, int64_t M, int32_t H,
+                                const int32_t* scatter_indx, int32_t k, const float* topk_weights, void* grad_y,
+                                float* grad_weights, void* stream) {
+    using namespace moe;
+    const TokArgs a{"moe_combine_tokens_backward", M, H, scatter_indx, k, stream};
+    const int rc = check(a, dtype, {grad_out, y, grad_y}, {scatter_indx, topk_weights, grad_weights});
+    if (rc != MOE_OK) return rc < 0 ? MOE_OK : rc;
+    MOE_TOK_DISPATCH(MOE_COMBINE_BWD, dtype, access_bytes<float>(H, grad_out, y, grad_y),
+                     access_bytes<__nv_bfloat16>(H, grad_out, y, grad_y), a, grad_out, y, topk_weights, grad_y,
+                     grad_weights);
+}
+
+}  // extern "C"

@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libmoe_routing.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 MOE_WEIGHT_K_BY_E, MOE_WEIGHT_E_BY_K = 0, 1
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -60,6 +62,19 @@ SIGNATURES = {
     "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
     "moe_expert_permutation": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                               _vp]),
+    "moe_gather_tokens": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _vp, _i32, _vp, _vp]),
+    "moe_gather_tokens_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _vp, _i32, _vp, _vp]),
+    "moe_combine_tokens": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "moe_combine_tokens_backward": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i32, _vp, _i32, _vp, _vp, _vp,
+                                                   _vp]),
+    "moe_expert_matmul": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, ctypes.c_int, _i32, _vp, _vp,
+                                         _vp, _vp]),
+    "moe_expert_matmul_grad_input": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, ctypes.c_int, _i32,
+                                                    _vp, _vp]),
+    "moe_expert_matmul_grad_weight": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, ctypes.c_int, _vp, _vp,
+                                                     _vp]),
+    "moe_topk_backward": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _i32, _i32, ctypes.c_int, _i32, _f32,
+                                         _f32, _vp, _vp]),
 }
 
 
