@@ -1,41 +1,96 @@
-// The experts' products over the segments of expert-sorted rows:
+// The experts' products over the segments of expert-sorted rows, on the
+// tcgen05 tensor cores:
 //
 //   moe_expert_matmul              out[p] = f(W_e x[p] + b_e) (gated: f(g) * u) + residual[p]
 //   moe_expert_matmul_grad_input   grad_x[p] = (W_e^T grad_out[p]) through f' at preact[p]
 //   moe_expert_matmul_grad_weight  grad_W_e = sum_p grad_out[p] x[p]^T, grad_b_e = sum_p grad_out[p]
 //
-// Simple form: 64 x 64 tiles on the CUDA cores, fp32 sums.
+// Two persistent kernels, one CTA per SM, warp-specialised: a TMA producer, an
+// MMA issuer and eight epilogue warps around a ring of shared-memory stages
+// and two TMEM accumulators, so that a tile's epilogue overlaps the next
+// tile's products.
+//
+// expert_rows_kernel (the first two calls).  A tile is 128 rows of the WEIGHT
+// times up to 256 tokens of one expert: the accumulator's 128 lanes are output
+// features and its columns tokens.  Segments have any length, and the column
+// count of tcgen05.mma goes in steps of 16, so a segment is cut into equal
+// parts of at most 256 tokens, rounded up to 16, instead of being padded to
+// 128 rows; and a handful of tokens costs one narrow product over weights that
+// stream past once.  grad_input differs only in the weight's orientation (its
+// tile is MN-major: reduction along the weight's rows).  A gated tile holds 64
+// gate and 64 up rows interleaved by 8, so that both factors of an output meet
+// in one thread's TMEM fragment.  The epilogue reads 16x256b fragments, works
+// in fp32, and turns them token-major with transposing matrix moves through
+// 80-byte shared-memory rows (a pitch without bank conflicts).
+//
+// expert_weight_kernel (grad_weight).  A tile is 128 x 256 of one expert's
+// gradient, both operands MN-major with the reduction along tokens.  The rows
+// behind a segment's end, which the last 64-row stage also brings, are zeroed
+// in shared memory before the product.
+//
+// Every wait is bounded; a wait that runs out is counted
+// (moe_watchdog_trips) and ends the block's work.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <cstdio>
+#include <mutex>
+#include <unordered_map>
 
+#include "expert_ptx.cuh"
 #include "moe_routing.h"
+#include "tma_host.cuh"
 
 namespace moe {
 
 int set_error(int status, const char* msg);
 int set_cuda_error(cudaError_t err, const char* what);
+int sm_count(int* dev, int* sms);
 
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kT = 64;
-constexpr int kKB = 16;
+constexpr int kMaxE = 1024;
+constexpr int kM = 128;                 // accumulator lanes: weight rows
+constexpr int kBK = 64;                 // reduction per stage (one 128-byte swizzle row)
+constexpr int kABytes = kM * kBK * 2;
+constexpr int kAccCols = 256;           // TMEM columns of one accumulator
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kPitch = 80;              // bytes of a staged token: 32 features and a bank shift
+constexpr int kEpiBytes = 32 * kPitch;  // per epilogue warp: 32 tokens
+constexpr uint64_t kWaitNs = 2000000000ull;
 
-struct MatArgs {
-    const bf16* x;       // forward: x; grad_input: grad_out; grad_weight: grad_out
-    const bf16* w;       // forward, grad_input: weight; grad_weight: x
+static __device__ unsigned int g_watchdog_trips_experts;
+
+enum Mode { kFwd, kFwdGated, kGrad, kGradGated };
+
+struct RowArgs {
     const int32_t* off;
     int64_t P;
-    int K, N, E;         // of the weight (N without the gate's doubling)
-    const float* bias;
-    int act, gated;
-    const bf16* extra;   // forward: residual; grad_input: preact
-    void* out;
+    int E;
+    int red;             // reduction length
+    int tiles_f;         // feature tiles
+    int tn_max;          // tokens per tile at most
+    int box;             // token rows per TMA copy
+    int stages, stage_bytes;
+    int N;               // columns of one output part
+    const float* bias;   // (E, N) or (E, 2 N)
+    int act;
+    const bf16* extra;   // forward: residual; gradient: preact
+    bf16* out;
     bf16* preact;
+};
+
+struct WeightArgs {
+    const int32_t* off;
+    int64_t P;
+    int E, N, K;
+    int tiles_n, tiles_k;
+    void* out;
     float* grad_bias;
 };
 
@@ -54,111 +109,776 @@ __device__ __forceinline__ float act_df(float z, int act) {
     return 1.0f;
 }
 
-__device__ __forceinline__ void segment(const MatArgs& a, int e, int64_t* begin, int64_t* end) {
-    const int64_t b = a.off[e], t = a.off[e + 1];
-    *begin = b < 0 ? 0 : b > a.P ? a.P : b;
-    *end = t < *begin ? *begin : t > a.P ? a.P : t;
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
-// blockIdx: x = column tile, y = row tiles of the expert in strides, z = expert.
-// GRAD false: D[p, n] = sum_k x[p, k] w[e, n, k]; true: D[p, k] = sum_n x[p, n] w[e, n, k].
-template <bool GRAD>
-__global__ void __launch_bounds__(256) simple_rows_kernel(MatArgs a) {
-    __shared__ float sa[kKB][kT + 1], sb[2][kKB][kT + 1];
-    int64_t begin, end;
-    segment(a, blockIdx.z, &begin, &end);
-    const int R = GRAD ? a.N : a.K;  // reduction length
-    const int C = GRAD ? a.K : a.N;  // output columns
-    const int nz = !GRAD && a.gated ? 2 : 1;
-    const int Nz = a.N * nz;
-    const bf16* w = a.w + (int64_t)blockIdx.z * Nz * a.K;
-    const int c0 = blockIdx.x * kT, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int64_t r0 = begin + (int64_t)blockIdx.y * kT; r0 < end; r0 += (int64_t)gridDim.y * kT) {
-        float acc[2][4][4] = {};
-        for (int k0 = 0; k0 < R; k0 += kKB) {
-            for (int i = threadIdx.x; i < kT * kKB; i += 256) {
-                const int r = i / kKB, kk = i % kKB;
-                sa[kk][r] = r0 + r < end && k0 + kk < R ? __bfloat162float(a.x[(r0 + r) * R + k0 + kk]) : 0.0f;
-                for (int h = 0; h < nz; ++h) {
-                    const int c = c0 + r;
-                    const bool in = c < C && k0 + kk < R;
-                    sb[h][kk][r] = !in ? 0.0f
-                                   : GRAD ? __bfloat162float(w[(int64_t)(k0 + kk) * a.K + c])
-                                          : __bfloat162float(w[((int64_t)h * a.N + c) * a.K + k0 + kk]);
-                }
-            }
-            __syncthreads();
-            for (int kk = 0; kk < kKB; ++kk)
-                for (int h = 0; h < nz; ++h)
-                    for (int i = 0; i < 4; ++i)
-                        for (int j = 0; j < 4; ++j)
-                            acc[h][i][j] = fmaf(sa[kk][ty * 4 + i], sb[h][kk][tx * 4 + j], acc[h][i][j]);
-            __syncthreads();
+__device__ __forceinline__ void give_up(volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicAdd(&g_watchdog_trips_experts, 1u);
+}
+
+// ---------------------------------------------------------------- segments
+// begin[e] and cum[e]: first row of expert e, and token tiles of the experts
+// before it.
+struct Segments {
+    int begin[kMaxE];
+    int count[kMaxE];
+    unsigned cum[kMaxE + 1];
+};
+
+__device__ __forceinline__ int tiles_of(int count, int tn_max) {
+    return (int)(((unsigned)count + tn_max - 1) / (unsigned)tn_max);
+}
+
+// All threads of the block; ends with a barrier.
+__device__ void load_segments(Segments& s, const int32_t* off, int E, int64_t P, int tn_max) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
+        const int64_t lo = b < 0 ? 0 : b > P ? P : b;
+        const int64_t hi = t > P ? P : t;
+        s.begin[e] = (int)lo;
+        s.count[e] = hi > lo ? (int)(hi - lo) : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int per = (E + 31) / 32, e0 = threadIdx.x * per;
+        unsigned long long mine = 0;
+        for (int e = e0; e < e0 + per && e < E; ++e) mine += tiles_of(s.count[e], tn_max);
+        unsigned long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((int)threadIdx.x >= o) incl += v;
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t r = r0 + ty * 4 + i;
-                const int c = c0 + tx * 4 + j;
-                if (r >= end || c >= C) continue;
-                if (GRAD) {
-                    const float q = acc[0][i][j];
-                    bf16* out = (bf16*)a.out;
-                    if (!a.extra) {
-                        out[r * C + c] = __float2bfloat16_rn(q);
-                    } else if (a.gated) {
-                        const float g = __bfloat162float(a.extra[r * 2 * C + c]);
-                        const float u = __bfloat162float(a.extra[r * 2 * C + C + c]);
-                        out[r * 2 * C + c] = __float2bfloat16_rn(q * u * act_df(g, a.act));
-                        out[r * 2 * C + C + c] = __float2bfloat16_rn(q * act_f(g, a.act));
-                    } else {
-                        out[r * C + c] = __float2bfloat16_rn(q * act_df(__bfloat162float(a.extra[r * C + c]), a.act));
-                    }
-                } else {
-                    float z[2] = {acc[0][i][j], acc[1][i][j]};
-                    for (int h = 0; h < nz; ++h) {
-                        if (a.bias) z[h] += a.bias[(int64_t)blockIdx.z * Nz + h * a.N + c];
-                        if (a.preact) a.preact[r * Nz + h * a.N + c] = __float2bfloat16_rn(z[h]);
-                    }
-                    float v = act_f(z[0], a.act);
-                    if (a.gated) v *= z[1];
-                    if (a.extra) v += __bfloat162float(a.extra[r * C + c]);
-                    ((bf16*)a.out)[r * C + c] = __float2bfloat16_rn(v);
-                }
-            }
+        unsigned at = (unsigned)(incl - mine);
+        for (int e = e0; e < e0 + per && e < E; ++e) {
+            s.cum[e] = at;
+            at += tiles_of(s.count[e], tn_max);
+        }
+        // Ranges that overlap so often that their tiles pass 32 bits are no
+        // permutation's: no tile at all.
+        if (threadIdx.x == 31) s.cum[E] = incl >> 31 ? 0u : (unsigned)incl;
+    }
+    __syncthreads();
+}
+
+struct Tile {
+    int e;      // expert
+    int f;      // feature tile
+    int row0;   // first token row
+    int valid;  // tokens of the tile
+    int tn;     // valid rounded up to 16
+};
+
+// Tiles run over experts, then feature tiles, then the token tiles of the
+// expert, so that neighbouring blocks share the weight's rows.
+__device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int64_t tile) {
+    int lo = 0, hi = a.E;  // cum[lo] * tiles_f <= tile < cum[hi] * tiles_f
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)s.cum[mid] * a.tiles_f <= tile) lo = mid;
+        else hi = mid;
+    }
+    Tile t;
+    t.e = lo;
+    const int parts = tiles_of(s.count[lo], a.tn_max);
+    const int64_t in = tile - (int64_t)s.cum[lo] * a.tiles_f;
+    t.f = (int)(in / parts);
+    const int part = (int)(in - (int64_t)t.f * parts);
+    const int step = ((s.count[lo] + parts - 1) / parts + 15) & ~15;
+    t.row0 = s.begin[lo] + part * step;
+    const int left = s.count[lo] - part * step;
+    t.valid = left < step ? left : step;
+    t.tn = (t.valid + 15) & ~15;
+    return t;
+}
+
+// ---------------------------------------------------------------- epilogue pieces
+// A warp's 32 tokens of `width` bytes each (features ascending), staged at
+// kPitch: 16-byte pieces between shared memory and rows of `ld` elements.
+// Pieces past `valid` tokens or past `cols` columns are skipped (or zero).
+template <int WIDTH>
+__device__ __forceinline__ void stage_to_global(const uint8_t* stage, bf16* dst, int64_t ld, int valid, int cols,
+                                                int lane) {
+    constexpr int PER = WIDTH / 16;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int idx = lane + 32 * i, tok = idx / PER, piece = idx % PER;
+        if (tok < valid && piece * 8 < cols)
+            *reinterpret_cast<uint4*>(dst + tok * ld + piece * 8) =
+                *reinterpret_cast<const uint4*>(stage + tok * kPitch + piece * 16);
     }
 }
 
-// blockIdx: x = K tile, y = N tile, z = expert.
-template <typename T>
-__global__ void __launch_bounds__(256) simple_weight_kernel(MatArgs a) {
-    __shared__ float sa[kKB][kT + 1], sb[kKB][kT + 1];
-    int64_t begin, end;
-    segment(a, blockIdx.z, &begin, &end);
-    const int n0 = blockIdx.y * kT, k0 = blockIdx.x * kT, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {}, sum = 0.0f;
-    for (int64_t p0 = begin; p0 < end; p0 += kKB) {
-        for (int i = threadIdx.x; i < kT * kKB; i += 256) {
-            const int pp = i / kT, c = i % kT;
-            const bool in = p0 + pp < end;
-            sa[pp][c] = in && n0 + c < a.N ? __bfloat162float(a.x[(p0 + pp) * a.N + n0 + c]) : 0.0f;
-            sb[pp][c] = in && k0 + c < a.K ? __bfloat162float(a.w[(p0 + pp) * a.K + k0 + c]) : 0.0f;
+template <int WIDTH>
+struct Rows {
+    uint4 v[WIDTH / 16];
+    __device__ __forceinline__ void load(const bf16* src, int64_t ld, int valid, int cols, int lane) {
+        constexpr int PER = WIDTH / 16;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = lane + 32 * i, tok = idx / PER, piece = idx % PER;
+            v[i] = tok < valid && piece * 8 < cols ? *reinterpret_cast<const uint4*>(src + tok * ld + piece * 8)
+                                                   : make_uint4(0, 0, 0, 0);
         }
-        __syncthreads();
-        for (int pp = 0; pp < kKB; ++pp) {
+    }
+    __device__ __forceinline__ void stage(uint8_t* stage, int lane) const {
+        constexpr int PER = WIDTH / 16;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = lane + 32 * i;
+            *reinterpret_cast<uint4*>(stage + (idx / PER) * kPitch + (idx % PER) * 16) = v[i];
+        }
+    }
+};
+
+// Fragments of 32 features x 32 tokens: w[i][m] holds tokens 8 i + 2 (l % 4) +
+// {0, 1} of feature 8 m + l / 4.
+__device__ __forceinline__ void put32(uint32_t stage, const uint32_t (&w)[4][4], int lane) {
+    const uint32_t at = stage + (lane % 8) * kPitch + (lane / 8) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::stmatrix_x4_trans(at + 8 * i * kPitch, w[i][0], w[i][1], w[i][2], w[i][3]);
+}
+__device__ __forceinline__ void get32(uint32_t stage, uint32_t (&w)[4][4], int lane) {
+    const uint32_t at = stage + (lane % 8) * kPitch + (lane / 8) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::ldmatrix_x4_trans(at + 8 * i * kPitch, w[i][0], w[i][1], w[i][2], w[i][3]);
+}
+// The same for 16 features (two 8-feature groups, two token groups a move).
+__device__ __forceinline__ void put16(uint32_t stage, const uint32_t (&w)[4][2], int lane) {
+    const uint32_t at = stage + ((lane / 16) * 8 + lane % 8) * kPitch + (lane / 8 % 2) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+        ptx::stmatrix_x4_trans(at + 8 * i * kPitch, w[i][0], w[i][1], w[i + 1][0], w[i + 1][1]);
+}
+__device__ __forceinline__ void get16(uint32_t stage, uint32_t (&w)[4][2], int lane) {
+    const uint32_t at = stage + ((lane / 16) * 8 + lane % 8) * kPitch + (lane / 8 % 2) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+        ptx::ldmatrix_x4_trans(at + 8 * i * kPitch, w[i][0], w[i][1], w[i + 1][0], w[i + 1][1]);
+}
+
+// One warp's 32 lanes x 32 tokens of the accumulator at taddr.
+template <int MODE>
+__device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, uint32_t taddr, int tok0, int quarter,
+                                               uint8_t* stage, int lane) {
+    constexpr int WIDTH = MODE == kFwdGated ? 32 : 64;       // bytes of one output part per token
+    const int valid = t.valid - tok0;                        // tokens of this chunk (may exceed 32)
+    const int col0 = MODE == kFwdGated ? t.f * 64 + quarter * 16 : t.f * kM + quarter * 32;
+    const int cols = a.N - col0;                             // columns left (may be <= 0)
+    const int64_t row0 = (int64_t)t.row0 + tok0;
+    const uint32_t sst = ptx::smem_u32(stage);
+
+    Rows<WIDTH> in0, in1;
+    const int64_t ld_in = MODE == kGradGated ? 2 * (int64_t)a.N : a.N;
+    if (a.extra != nullptr) {
+        in0.load(a.extra + row0 * ld_in + col0, ld_in, valid, cols, lane);
+        if constexpr (MODE == kGradGated) in1.load(a.extra + row0 * ld_in + a.N + col0, ld_in, valid, cols, lane);
+    }
+    float acc[2][4][4];
+    ptx::tmem_ld_frag32(taddr, acc);
+
+    if constexpr (MODE == kFwd) {
+        uint32_t w[4][4];
+        if (a.bias != nullptr) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int c = 8 * m + lane / 4;
+                const float b = c < cols ? __ldg(a.bias + (int64_t)t.e * a.N + col0 + c) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[m / 2][i][2 * (m % 2)] += b;
+                    acc[m / 2][i][2 * (m % 2) + 1] += b;
+                }
+            }
+        }
+        if (a.preact != nullptr) {
+#pragma unroll
             for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[pp][ty * 4 + i], sb[pp][tx * 4 + j], acc[i][j]);
-            if (threadIdx.x < kT) sum += sa[pp][threadIdx.x];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) w[i][m] = pack(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]);
+            put32(sst, w, lane);
+            __syncwarp();
+            stage_to_global<64>(stage, a.preact + row0 * a.N + col0, a.N, valid, cols, lane);
+            __syncwarp();
         }
-        __syncthreads();
+        uint32_t r[4][4];
+        if (a.extra != nullptr) {
+            in0.stage(stage, lane);
+            __syncwarp();
+            get32(sst, r, lane);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float x = act_f(acc[m / 2][i][2 * (m % 2)], a.act), y = act_f(acc[m / 2][i][2 * (m % 2) + 1], a.act);
+                if (a.extra != nullptr) {
+                    const float2 q = unpack(r[i][m]);
+                    x += q.x;
+                    y += q.y;
+                }
+                w[i][m] = pack(x, y);
+            }
+        put32(sst, w, lane);
+        __syncwarp();
+        stage_to_global<64>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
+    } else if constexpr (MODE == kFwdGated) {
+        const int64_t ld_z = 2 * (int64_t)a.N;
+        if (a.bias != nullptr) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = 8 * h + lane / 4;
+                const float* b = a.bias + (int64_t)t.e * ld_z + col0 + c;
+                const float bg = c < cols ? __ldg(b) : 0.0f, bu = c < cols ? __ldg(b + a.N) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[h][i][0] += bg;
+                    acc[h][i][1] += bg;
+                    acc[h][i][2] += bu;
+                    acc[h][i][3] += bu;
+                }
+            }
+        }
+        uint32_t w[4][2];
+        if (a.preact != nullptr) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) w[i][h] = pack(acc[h][i][2 * part], acc[h][i][2 * part + 1]);
+                put16(sst, w, lane);
+                __syncwarp();
+                stage_to_global<32>(stage, a.preact + row0 * ld_z + part * a.N + col0, ld_z, valid, cols, lane);
+                __syncwarp();
+            }
+        }
+        uint32_t r[4][2];
+        if (a.extra != nullptr) {
+            in0.stage(stage, lane);
+            __syncwarp();
+            get16(sst, r, lane);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = act_f(acc[h][i][0], a.act) * acc[h][i][2], y = act_f(acc[h][i][1], a.act) * acc[h][i][3];
+                if (a.extra != nullptr) {
+                    const float2 q = unpack(r[i][h]);
+                    x += q.x;
+                    y += q.y;
+                }
+                w[i][h] = pack(x, y);
+            }
+        put16(sst, w, lane);
+        __syncwarp();
+        stage_to_global<32>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
+    } else {
+        uint32_t w[4][4], g[4][4], u[4][4];
+        if (a.extra != nullptr) {
+            in0.stage(stage, lane);
+            __syncwarp();
+            get32(sst, g, lane);
+            __syncwarp();
+            if constexpr (MODE == kGradGated) {
+                in1.stage(stage, lane);
+                __syncwarp();
+                get32(sst, u, lane);
+                __syncwarp();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float x = acc[m / 2][i][2 * (m % 2)], y = acc[m / 2][i][2 * (m % 2) + 1];
+                if (a.extra != nullptr) {
+                    const float2 z = unpack(g[i][m]);
+                    if constexpr (MODE == kGradGated) {
+                        const float2 v = unpack(u[i][m]);
+                        u[i][m] = pack(x * act_f(z.x, a.act), y * act_f(z.y, a.act));
+                        x *= v.x;
+                        y *= v.y;
+                    }
+                    x *= act_df(z.x, a.act);
+                    y *= act_df(z.y, a.act);
+                }
+                w[i][m] = pack(x, y);
+            }
+        put32(sst, w, lane);
+        __syncwarp();
+        stage_to_global<64>(stage, a.out + row0 * ld_in + col0, ld_in, valid, cols, lane);
+        if constexpr (MODE == kGradGated) {
+            __syncwarp();
+            put32(sst, u, lane);
+            __syncwarp();
+            stage_to_global<64>(stage, a.out + row0 * ld_in + a.N + col0, ld_in, valid, cols, lane);
+        }
     }
-    T* out = static_cast<T*>(a.out) + (int64_t)blockIdx.z * a.N * a.K;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + ty * 4 + i, k = k0 + tx * 4 + j;
-            if (n < a.N && k < a.K) out[(int64_t)n * a.K + k] = T(acc[i][j]);
+    __syncwarp();
+}
+
+// Shared-memory layout behind the stage ring.
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+__device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(&c->full[s], 1);
+            ptx::mbar_init(&c->empty[s], 1);
         }
-    if (a.grad_bias && blockIdx.x == 0 && threadIdx.x < kT && n0 + (int)threadIdx.x < a.N)
-        a.grad_bias[(int64_t)blockIdx.z * a.N + n0 + threadIdx.x] = sum;
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&c->acc_full[b], 1);
+            ptx::mbar_init(&c->acc_empty[b], kEpiWarps);
+        }
+        c->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc(&c->tmem, 2 * kAccCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    return c->tmem;
+}
+
+__device__ __forceinline__ void end_block(uint32_t tmem, int warp) {
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 2 * kAccCols);
+    }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, RowArgs a) {
+    constexpr bool GRAD = MODE == kGrad || MODE == kGradGated;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = ptx::smem_align<1024>(smem_raw);
+    uint8_t* epi = ring + a.stages * a.stage_bytes;
+    Control* c = reinterpret_cast<Control*>(epi + kEpiWarps * kEpiBytes);
+    Segments& seg = *reinterpret_cast<Segments*>(c + 1);
+    volatile int* abort_flag = &c->abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ptx::tma_prefetch_desc(&tmW);
+        ptx::tma_prefetch_desc(&tmX);
+    }
+    const uint32_t tmem = start_block(c, a.stages, warp);
+    ptx::griddep_wait();
+    load_segments(seg, a.off, a.E, a.P, a.tn_max);
+    const int64_t tiles = (int64_t)seg.cum[a.E] * a.tiles_f;
+    const int nkb = (a.red + kBK - 1) / kBK;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int kb_all = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const Tile t = tile_at(seg, a, tile);
+                const int boxes = (t.tn + a.box - 1) / a.box;
+                const uint32_t bytes = kABytes + boxes * a.box * kBK * 2;
+                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
+                    const int s = kb_all % a.stages;
+                    if (*abort_flag || !ptx::mbar_wait(&c->empty[s], ((kb_all / a.stages) & 1) ^ 1, kWaitNs)) {
+                        give_up(abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* a_s = ring + s * a.stage_bytes;
+                    uint8_t* b_s = a_s + kABytes;
+                    ptx::mbar_arrive_expect_tx(&c->full[s], bytes);
+                    if constexpr (GRAD) {
+                        ptx::tma_load(a_s, &tmW, t.f * kM, kb * kBK, t.e, &c->full[s]);
+                        ptx::tma_load(a_s + kABytes / 2, &tmW, t.f * kM + 64, kb * kBK, t.e, &c->full[s]);
+                    } else if constexpr (MODE == kFwdGated) {
+                        ptx::tma_load(a_s, &tmW, kb * kBK, 0, 0, t.f * 8, t.e, &c->full[s]);
+                    } else {
+                        ptx::tma_load(a_s, &tmW, kb * kBK, t.f * kM, t.e, &c->full[s]);
+                    }
+                    for (int i = 0; i < boxes; ++i)
+                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, kb * kBK, t.row0 + i * a.box, &c->full[s]);
+                }
+            }
+            // Leave only once the copies issued have landed (bounded).
+            for (int k = 0; k < a.stages && k < kb_all; ++k) {
+                const int j = kb_all - 1 - k;
+                ptx::mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int kb_all = 0, n = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++n) {
+                const Tile t = tile_at(seg, a, tile);
+                const uint32_t idesc = ptx::idesc_bf16_m128(t.tn, GRAD, false);
+                const int b = n & 1;
+                if (!ptx::mbar_wait(&c->acc_empty[b], ((n >> 1) & 1) ^ 1, kWaitNs)) {
+                    give_up(abort_flag);
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + b * kAccCols;
+                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
+                    const int s = kb_all % a.stages;
+                    if (*abort_flag || !ptx::mbar_wait(&c->full[s], (kb_all / a.stages) & 1, kWaitNs)) {
+                        give_up(abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a_addr = ptx::smem_u32(ring + s * a.stage_bytes);
+                    const uint32_t b_addr = a_addr + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        const uint64_t ad = GRAD ? ptx::sdesc_sw128(a_addr + kk * 2048, kABytes / 2, 1024)
+                                                 : ptx::sdesc_sw128(a_addr + kk * 32, 16, 1024);
+                        ptx::umma_bf16(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc, (kb | kk) != 0);
+                    }
+                    ptx::umma_commit(&c->empty[s]);
+                }
+                ptx::umma_commit(&c->acc_full[b]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        uint8_t* stage = epi + ew * kEpiBytes;
+        int n = 0;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+            const Tile t = tile_at(seg, a, tile);
+            const int b = n & 1;
+            if (!ptx::mbar_wait(&c->acc_full[b], (n >> 1) & 1, kWaitNs)) {
+                if (lane == 0) give_up(abort_flag);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+            if (*abort_flag) break;
+            ptx::tc_fence_after();
+            const uint32_t base = tmem + b * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+            for (int tok0 = half * 32; tok0 < t.valid; tok0 += 64)
+                epilogue_chunk<MODE>(a, t, base + tok0, tok0, quarter, stage, lane);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&c->acc_empty[b]);
+        }
+    }
+    __syncwarp();
+    end_block(tmem, warp);
+}
+
+// ---------------------------------------------------------------- weight gradient
+constexpr int kWN = 256;                          // columns of a tile (K side)
+constexpr int kWStages = 4;
+constexpr int kWStageBytes = kABytes + kWN * kBK * 2;
+
+template <typename T>
+__device__ __forceinline__ void store32(T* dst, const float (&v)[32], int cols) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            if (i < cols) *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            if (i < cols)
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack(v[i], v[i + 1]), pack(v[i + 2], v[i + 3]),
+                                                               pack(v[i + 4], v[i + 5]), pack(v[i + 6], v[i + 7]));
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_weight_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
+                         WeightArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = ptx::smem_align<1024>(smem_raw);
+    Control* c = reinterpret_cast<Control*>(ring + kWStages * kWStageBytes);
+    Segments& seg = *reinterpret_cast<Segments*>(c + 1);
+    volatile int* abort_flag = &c->abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ptx::tma_prefetch_desc(&tmY);
+        ptx::tma_prefetch_desc(&tmX);
+    }
+    const uint32_t tmem = start_block(c, kWStages, warp);
+    ptx::griddep_wait();
+    load_segments(seg, a.off, a.E, a.P, kBK);
+    const int per_e = a.tiles_n * a.tiles_k;
+    const int64_t tiles = (int64_t)a.E * per_e;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int kb_all = 0;
+            bool ok = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
+                const int n0 = in / a.tiles_k * kM, k0 = in % a.tiles_k * kWN;
+                const int nkb = tiles_of(seg.count[e], kBK);
+                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
+                    const int s = kb_all % kWStages;
+                    if (*abort_flag || !ptx::mbar_wait(&c->empty[s], ((kb_all / kWStages) & 1) ^ 1, kWaitNs)) {
+                        give_up(abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* a_s = ring + s * kWStageBytes;
+                    const int row = seg.begin[e] + kb * kBK;
+                    ptx::mbar_arrive_expect_tx(&c->full[s], kWStageBytes);
+#pragma unroll
+                    for (int i = 0; i < kM / 64; ++i)
+                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, &c->full[s]);
+#pragma unroll
+                    for (int i = 0; i < kWN / 64; ++i)
+                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, &c->full[s]);
+                }
+            }
+            for (int k = 0; k < kWStages && k < kb_all; ++k) {
+                const int j = kb_all - 1 - k;
+                ptx::mbar_wait(&c->full[j % kWStages], (j / kWStages) & 1, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = ptx::idesc_bf16_m128(kWN, true, true);
+        int kb_all = 0, n = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const int e = (int)(tile / per_e);
+            const int count = seg.count[e], nkb = tiles_of(count, kBK);
+            if (nkb == 0) continue;
+            const int b = n & 1;
+            if (!ptx::mbar_wait(&c->acc_empty[b], ((n >> 1) & 1) ^ 1, kWaitNs)) {
+                if (lane == 0) give_up(abort_flag);
+                break;
+            }
+            ++n;
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + b * kAccCols;
+            for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
+                const int s = kb_all % kWStages;
+                if (!ptx::mbar_wait(&c->full[s], (kb_all / kWStages) & 1, kWaitNs)) {
+                    if (lane == 0) give_up(abort_flag);
+                    ok = false;
+                    break;
+                }
+                uint8_t* a_s = ring + s * kWStageBytes;
+                const int left = count - kb * kBK;           // rows of the segment in this stage
+                const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
+                if (left < kBK) {
+                    // rows [left, 16 * steps) of all six boxes are the next segment's: zero them
+                    const int pieces = (16 * steps - left) * 8;  // 16-byte pieces per box
+                    for (int i = lane; i < pieces * (kWStageBytes / 8192); i += 32)
+                        *reinterpret_cast<uint4*>(a_s + (i / pieces) * 8192 + left * 128 + (i % pieces) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    ptx::fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+                    const uint32_t a_addr = ptx::smem_u32(a_s), b_addr = a_addr + kABytes;
+                    for (int kk = 0; kk < steps; ++kk)
+                        ptx::umma_bf16(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
+                                       ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc, (kb | kk) != 0);
+                    ptx::umma_commit(&c->empty[s]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) ptx::umma_commit(&c->acc_full[b]);
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        int n = 0;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
+            const int row = in / a.tiles_k * kM + quarter * 32 + lane, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
+            const bool some = seg.count[e] > 0;
+            const int b = n & 1;
+            if (some) {
+                if (!ptx::mbar_wait(&c->acc_full[b], (n >> 1) & 1, kWaitNs)) {
+                    if (lane == 0) give_up(abort_flag);
+                    *abort_flag = 1;
+                }
+                ++n;
+                __syncwarp();
+                if (*abort_flag) break;
+                ptx::tc_fence_after();
+            }
+            const uint32_t base =
+                tmem + b * kAccCols + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
+            T* out = static_cast<T*>(a.out) + ((int64_t)e * a.N + row) * a.K + k0;
+#pragma unroll 1
+            for (int j = 0; j < kWN / 2; j += 32) {
+                float v[32];
+                if (some) {
+                    ptx::tmem_ld32(base + j, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                }
+                if (row < a.N) store32(out + j, v, a.K - k0 - j);
+                __syncwarp();
+            }
+            if (some) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&c->acc_empty[b]);
+            }
+        }
+    }
+    __syncwarp();
+    end_block(tmem, warp);
+}
+
+// Column sums of the segments: a block per (expert, 256 columns), its eight
+// warps over rows in steps of 8, joined in warp order.
+__global__ void __launch_bounds__(256)
+    expert_bias_kernel(const bf16* dy, const int32_t* off, int64_t P, int N, float* grad_bias) {
+    __shared__ float part[8][256];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.y, c = blockIdx.x * 256 + lane * 8;
+    ptx::griddep_wait();
+    const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
+    const int64_t lo = b < 0 ? 0 : b > P ? P : b, hi = t > P ? P : t;
+    float s[8] = {};
+    if (c < N)
+        for (int64_t r = lo + warp; r < hi; r += 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(dy + r * N + c);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack(w[i]);
+                s[2 * i] += f.x;
+                s[2 * i + 1] += f.y;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[warp][lane * 8 + i] = s[i];
+    __syncthreads();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col < N) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += part[w][threadIdx.x];
+        grad_bias[(int64_t)e * N + col] = sum;
+    }
+}
+
+// ---------------------------------------------------------------- host
+// A bf16 tensor of `rank` dimensions, innermost first; strides in elements.
+cudaError_t encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box) {
+    using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    static cudaError_t status = cudaSuccess;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        status = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+        if (status == cudaSuccess && q != cudaDriverEntryPointSuccess) status = cudaErrorNotSupported;
+        fn = reinterpret_cast<EncodeFn>(p);
+    });
+    if (status != cudaSuccess || fn == nullptr) return status == cudaSuccess ? cudaErrorNotSupported : status;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i > 0) st[i - 1] = strides[i - 1] * 2;
+    }
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)cols};
+    const uint32_t box[2] = {64, (uint32_t)box_rows};
+    return encode(map, base, 2, dims, strides, box);
+}
+
+// Dynamic shared memory allowed for a kernel on the current device, once.
+int allow_smem(const void* kern, int dev, size_t bytes) {
+    static std::mutex mu;
+    static std::unordered_map<int, std::unordered_map<const void*, bool>> done;  // device -> kernel
+    std::lock_guard<std::mutex> lk(mu);
+    bool& set = done[dev][kern];
+    if (set) return MOE_OK;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (err != cudaSuccess) return set_cuda_error(err, "cudaFuncSetAttribute(expert matmul smem)");
+    set = true;
+    return MOE_OK;
+}
+
+template <typename... KArgs, typename... Args>
+int launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, const char* who, void* stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, args...);
+    return err == cudaSuccess ? MOE_OK : set_cuda_error(err, who);
+}
+
+constexpr size_t kSmemMax = 232448;  // 227 KB
+constexpr size_t kTail = kEpiWarps * kEpiBytes + sizeof(Control) + sizeof(Segments);
+constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + sizeof(Control) + sizeof(Segments);
+static_assert(kWeightSmem <= kSmemMax, "weight gradient's shared memory");
+static_assert(1024 + 4 * (kABytes + 256 * kBK * 2) + kTail <= kSmemMax, "row products' shared memory");
+
+// Tokens per tile, by the experts' mean share of rows: narrow tiles leave
+// room for more stages, which a product that waits for its weights needs.
+void choose_tile(RowArgs& a) {
+    const int64_t mean = (a.P + a.E - 1) / a.E;
+    a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
+    a.box = a.tn_max <= 64 ? 16 : a.tn_max / 4;
+    a.stage_bytes = kABytes + a.tn_max * kBK * 2;
+    const int fit = (int)((kSmemMax - 1024 - kTail) / a.stage_bytes);
+    a.stages = fit < kMaxStages ? fit : kMaxStages;
+}
+
+template <int MODE>
+int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_cols, RowArgs& a, void* stream) {
+    int dev = 0, sms = 0;
+    int rc = sm_count(&dev, &sms);
+    if (rc != MOE_OK) return rc;
+    rc = allow_smem((const void*)expert_rows_kernel<MODE>, dev, kSmemMax);
+    if (rc != MOE_OK) return rc;
+    CUtensorMap tmX;
+    cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, a.box);
+    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
+    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kTail;
+    return launch(expert_rows_kernel<MODE>, dim3(sms), kThreads, smem, who, stream, tmW, tmX, a);
 }
 
 bool bad(const void* p, size_t n) { return !p || reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -194,17 +914,16 @@ int bad_pointer(const char* who) {
     return set_error(MOE_ERR_INVALID_ARG, msg);
 }
 
-int row_tiles(int64_t P) {
-    const int64_t t = (P + kT - 1) / kT;
-    return (int)(t < 64 ? t : 64);
-}
-
-int launched(const char* who) {
-    cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? MOE_OK : set_cuda_error(err, who);
-}
-
 }  // namespace
+
+int read_expert_watchdog(unsigned int* count) {
+    unsigned int v = 0;
+    cudaError_t err = cudaMemcpyFromSymbol(&v, g_watchdog_trips_experts, sizeof(v));
+    if (err != cudaSuccess) return set_cuda_error(err, "cudaMemcpyFromSymbol(expert watchdog)");
+    *count = v;
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 extern "C" {
@@ -220,10 +939,34 @@ int moe_expert_matmul(const void* x, const void* weight, const int32_t* expert_o
     if (bad(x, 16) || bad(weight, 16) || bad(expert_offsets, 4) || bad_opt(bias, 4) || bad_opt(residual, 16) ||
         bad(out, 16) || bad_opt(preact_out, 16))
         return bad_pointer(who);
-    MatArgs a{(const bf16*)x, (const bf16*)weight, expert_offsets, P, K, N, E, bias, activation, gated,
-              (const bf16*)residual, out, (bf16*)preact_out, nullptr};
-    simple_rows_kernel<false><<<dim3((N + kT - 1) / kT, row_tiles(P), E), 256, 0, (cudaStream_t)stream>>>(a);
-    return launched(who);
+    RowArgs a = {};
+    a.off = expert_offsets;
+    a.P = P;
+    a.E = E;
+    a.red = K;
+    a.N = N;
+    a.tiles_f = gated ? (N + 63) / 64 : (N + kM - 1) / kM;
+    a.bias = bias;
+    a.act = activation;
+    a.extra = (const bf16*)residual;
+    a.out = (bf16*)out;
+    a.preact = (bf16*)preact_out;
+    choose_tile(a);
+    CUtensorMap tmW;
+    cudaError_t err;
+    const uint64_t k = K, n = N;
+    if (gated) {
+        // rows in the order (block of 8, gate or up, row of the block)
+        const uint64_t dims[5] = {k, 8, 2, n / 8, (uint64_t)E}, strides[4] = {k, n * k, 8 * k, 2 * n * k};
+        const uint32_t box[5] = {64, 8, 2, 8, 1};
+        err = encode(&tmW, weight, 5, dims, strides, box);
+    } else {
+        const uint64_t dims[3] = {k, n, (uint64_t)E}, strides[2] = {k, n * k};
+        const uint32_t box[3] = {64, kM, 1};
+        err = encode(&tmW, weight, 3, dims, strides, box);
+    }
+    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(weight)");
+    return gated ? run_rows<kFwdGated>(who, tmW, x, K, a, stream) : run_rows<kFwd>(who, tmW, x, K, a, stream);
 }
 
 int moe_expert_matmul_grad_input(const void* grad_out, const void* weight, const int32_t* expert_offsets, int64_t P,
@@ -238,10 +981,24 @@ int moe_expert_matmul_grad_input(const void* grad_out, const void* weight, const
     if (P == 0) return MOE_OK;
     if (bad(grad_out, 16) || bad(weight, 16) || bad(expert_offsets, 4) || bad_opt(preact, 16) || bad(grad_x, 16))
         return bad_pointer(who);
-    MatArgs a{(const bf16*)grad_out, (const bf16*)weight, expert_offsets, P, K, N, E, nullptr, activation, gated,
-              (const bf16*)preact, grad_x, nullptr, nullptr};
-    simple_rows_kernel<true><<<dim3((K + kT - 1) / kT, row_tiles(P), E), 256, 0, (cudaStream_t)stream>>>(a);
-    return launched(who);
+    RowArgs a = {};
+    a.off = expert_offsets;
+    a.P = P;
+    a.E = E;
+    a.red = N;
+    a.N = K;
+    a.tiles_f = (K + kM - 1) / kM;
+    a.act = activation;
+    a.extra = (const bf16*)preact;
+    a.out = (bf16*)grad_x;
+    choose_tile(a);
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)K, (uint64_t)N * K};
+    const uint32_t box[3] = {64, kBK, 1};
+    CUtensorMap tmW;
+    cudaError_t err = encode(&tmW, weight, 3, dims, strides, box);
+    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(weight)");
+    return gated ? run_rows<kGradGated>(who, tmW, grad_out, N, a, stream)
+                 : run_rows<kGrad>(who, tmW, grad_out, N, a, stream);
 }
 
 int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int32_t* expert_offsets, int64_t P,
@@ -257,14 +1014,27 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     if ((P > 0 && (bad(grad_out, 16) || bad(x, 16))) || bad(expert_offsets, 4) || bad(grad_weight, 16) ||
         bad_opt(grad_bias, 4))
         return bad_pointer(who);
-    MatArgs a{(const bf16*)grad_out, (const bf16*)x, expert_offsets, P, K, N, E, nullptr, 0, 0, nullptr,
-              grad_weight, nullptr, grad_bias};
-    const dim3 grid((K + kT - 1) / kT, (N + kT - 1) / kT, E);
-    if (dtype == MOE_DTYPE_F32)
-        simple_weight_kernel<float><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
-    else
-        simple_weight_kernel<bf16><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
-    return launched(who);
+    int dev = 0, sms = 0;
+    int rc2 = sm_count(&dev, &sms);
+    if (rc2 != MOE_OK) return rc2;
+    WeightArgs a = {expert_offsets, P, E, N, K, (N + kM - 1) / kM, (K + kWN - 1) / kWN, grad_weight, grad_bias};
+    CUtensorMap tmY, tmX;
+    // with P == 0 nothing is read through the maps; they still have to be valid ones
+    cudaError_t err = encode_rows(&tmY, P ? grad_out : grad_weight, P ? P : 1, N, kBK);
+    if (err == cudaSuccess) err = encode_rows(&tmX, P ? x : grad_weight, P ? P : 1, K, kBK);
+    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
+    if (dtype == MOE_DTYPE_F32) {
+        rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kWeightSmem);
+        if (rc2 == MOE_OK)
+            rc2 = launch(expert_weight_kernel<float>, dim3(sms), kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+    } else {
+        rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kWeightSmem);
+        if (rc2 == MOE_OK)
+            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms), kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+    }
+    if (rc2 != MOE_OK || !grad_bias) return rc2;
+    return launch(expert_bias_kernel, dim3((N + 255) / 256, E), 256, 0, who, stream, (const bf16*)grad_out,
+                  expert_offsets, P, (int)N, grad_bias);
 }
 
 }  // extern "C"

@@ -306,11 +306,16 @@ int launch_fused_decode(const CUtensorMap& tmA, const void* router_weight, bool 
     return grouped ? launch_decode_route<false, true>(ra, st) : launch_decode_route<false, false>(ra, st);
 }
 
+int read_expert_watchdog(unsigned int* count);  // the experts' products
+
+// Trips of the two-launch decode path and of the experts' products.
 int read_decode_watchdog(unsigned int* count) {
-    unsigned int v = 0;
+    unsigned int v = 0, w = 0;
     cudaError_t err = cudaMemcpyFromSymbol(&v, g_watchdog_trips_decode, sizeof(v));
     if (err != cudaSuccess) return set_cuda_error(err, "cudaMemcpyFromSymbol(decode watchdog)");
-    *count = v;
+    const int rc = read_expert_watchdog(&w);
+    if (rc != MOE_OK) return rc;
+    *count = v + w;
     return MOE_OK;
 }
 
