@@ -94,15 +94,16 @@ struct WeightArgs {
     float* grad_bias;
 };
 
+// The intrinsics' few units in the 24th bit vanish in the rounding to bf16.
 __device__ __forceinline__ float act_f(float z, int act) {
-    if (act == MOE_ACT_SILU) return z / (1.0f + expf(-z));
+    if (act == MOE_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
     if (act == MOE_ACT_GELU) return z * normcdff(z);
     return z;
 }
 
 __device__ __forceinline__ float act_df(float z, int act) {
     if (act == MOE_ACT_SILU) {
-        const float p = 1.0f / (1.0f + expf(-z));
+        const float p = __fdividef(1.0f, 1.0f + __expf(-z));
         return p * (1.0f + z * (1.0f - p));
     }
     if (act == MOE_ACT_GELU) return normcdff(z) + z * 0.3989422804014327f * expf(-0.5f * z * z);
@@ -115,6 +116,26 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// Position in a ring of `n` barriers: index and phase parity, stepped without
+// division (a division by the runtime stage count costs an issuing lane more
+// than the four products of a stage).
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n) {
+        if (++s == n) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void give_up(volatile int* abort_flag) {
@@ -282,9 +303,10 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
     }
     float acc[2][4][4];
     ptx::tmem_ld_frag32(taddr, acc);
+    const int groups = valid >= 32 ? 4 : (valid + 7) / 8;    // token groups of 8 in use
 
     if constexpr (MODE == kFwd) {
-        uint32_t w[4][4];
+        uint32_t w[4][4] = {};
         if (a.bias != nullptr) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -315,7 +337,8 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             __syncwarp();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            if (i >= groups) break;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float x = act_f(acc[m / 2][i][2 * (m % 2)], a.act), y = act_f(acc[m / 2][i][2 * (m % 2) + 1], a.act);
@@ -326,6 +349,7 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 }
                 w[i][m] = pack(x, y);
             }
+        }
         put32(sst, w, lane);
         __syncwarp();
         stage_to_global<64>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
@@ -346,7 +370,7 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 }
             }
         }
-        uint32_t w[4][2];
+        uint32_t w[4][2] = {};
         if (a.preact != nullptr) {
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -368,7 +392,8 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             __syncwarp();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            if (i >= groups) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x = act_f(acc[h][i][0], a.act) * acc[h][i][2], y = act_f(acc[h][i][1], a.act) * acc[h][i][3];
@@ -379,11 +404,12 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 }
                 w[i][h] = pack(x, y);
             }
+        }
         put16(sst, w, lane);
         __syncwarp();
         stage_to_global<32>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
     } else {
-        uint32_t w[4][4], g[4][4], u[4][4];
+        uint32_t w[4][4] = {}, g[4][4], u[4][4] = {};
         if (a.extra != nullptr) {
             in0.stage(stage, lane);
             __syncwarp();
@@ -397,7 +423,8 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            if (i >= groups) break;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float x = acc[m / 2][i][2 * (m % 2)], y = acc[m / 2][i][2 * (m % 2) + 1];
@@ -414,6 +441,7 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 }
                 w[i][m] = pack(x, y);
             }
+        }
         put32(sst, w, lane);
         __syncwarp();
         stage_to_global<64>(stage, a.out + row0 * ld_in + col0, ld_in, valid, cols, lane);
@@ -486,99 +514,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::griddep_wait();
     load_segments(seg, a.off, a.E, a.P, a.tn_max);
     const int64_t tiles = (int64_t)seg.cum[a.E] * a.tiles_f;
-    const int nkb = (a.red + kBK - 1) / kBK;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int kb_all = 0;
+        if (elect_one()) {
+            Ring r;
             bool ok = true;
             for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 const Tile t = tile_at(seg, a, tile);
                 const int boxes = (t.tn + a.box - 1) / a.box;
                 const uint32_t bytes = kABytes + boxes * a.box * kBK * 2;
-                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
-                    const int s = kb_all % a.stages;
-                    if (*abort_flag || !ptx::mbar_wait(&c->empty[s], ((kb_all / a.stages) & 1) ^ 1, kWaitNs)) {
+                for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
+                    if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
-                    uint8_t* a_s = ring + s * a.stage_bytes;
+                    uint8_t* a_s = ring + r.s * a.stage_bytes;
                     uint8_t* b_s = a_s + kABytes;
-                    ptx::mbar_arrive_expect_tx(&c->full[s], bytes);
+                    uint64_t* full = &c->full[r.s];
+                    ptx::mbar_arrive_expect_tx(full, bytes);
                     if constexpr (GRAD) {
-                        ptx::tma_load(a_s, &tmW, t.f * kM, kb * kBK, t.e, &c->full[s]);
-                        ptx::tma_load(a_s + kABytes / 2, &tmW, t.f * kM + 64, kb * kBK, t.e, &c->full[s]);
+                        ptx::tma_load(a_s, &tmW, t.f * kM, k, t.e, full);
+                        ptx::tma_load(a_s + kABytes / 2, &tmW, t.f * kM + 64, k, t.e, full);
                     } else if constexpr (MODE == kFwdGated) {
-                        ptx::tma_load(a_s, &tmW, kb * kBK, 0, 0, t.f * 8, t.e, &c->full[s]);
+                        ptx::tma_load(a_s, &tmW, k, 0, 0, t.f * 8, t.e, full);
                     } else {
-                        ptx::tma_load(a_s, &tmW, kb * kBK, t.f * kM, t.e, &c->full[s]);
+                        ptx::tma_load(a_s, &tmW, k, t.f * kM, t.e, full);
                     }
                     for (int i = 0; i < boxes; ++i)
-                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, kb * kBK, t.row0 + i * a.box, &c->full[s]);
+                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, k, t.row0 + i * a.box, full);
                 }
             }
-            // Leave only once the copies issued have landed (bounded).
-            for (int k = 0; k < a.stages && k < kb_all; ++k) {
-                const int j = kb_all - 1 - k;
-                ptx::mbar_wait(&c->full[j % a.stages], (j / a.stages) & 1, kWaitNs);
-            }
+            // Leave only once every stage filled has been used, or its wait has run out.
+            for (int i = 0; i < a.stages; ++i, r.step(a.stages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int kb_all = 0, n = 0;
+        if (elect_one()) {
+            Ring r, acc;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++n) {
+            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, acc.step(2)) {
                 const Tile t = tile_at(seg, a, tile);
                 const uint32_t idesc = ptx::idesc_bf16_m128(t.tn, GRAD, false);
-                const int b = n & 1;
-                if (!ptx::mbar_wait(&c->acc_empty[b], ((n >> 1) & 1) ^ 1, kWaitNs)) {
+                if (!ptx::mbar_wait(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
                     give_up(abort_flag);
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t d = tmem + b * kAccCols;
-                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
-                    const int s = kb_all % a.stages;
-                    if (*abort_flag || !ptx::mbar_wait(&c->full[s], (kb_all / a.stages) & 1, kWaitNs)) {
+                const uint32_t d = tmem + acc.s * kAccCols;
+                for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
+                    if (!ptx::mbar_wait(&c->full[r.s], r.phase, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t a_addr = ptx::smem_u32(ring + s * a.stage_bytes);
+                    const uint32_t a_addr = ptx::smem_u32(ring + r.s * a.stage_bytes);
                     const uint32_t b_addr = a_addr + kABytes;
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk) {
                         const uint64_t ad = GRAD ? ptx::sdesc_sw128(a_addr + kk * 2048, kABytes / 2, 1024)
                                                  : ptx::sdesc_sw128(a_addr + kk * 32, 16, 1024);
-                        ptx::umma_bf16(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc, (kb | kk) != 0);
+                        ptx::umma_bf16(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc, (k | kk) != 0);
                     }
-                    ptx::umma_commit(&c->empty[s]);
+                    ptx::umma_commit(&c->empty[r.s]);
                 }
-                ptx::umma_commit(&c->acc_full[b]);
+                ptx::umma_commit(&c->acc_full[acc.s]);
             }
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         uint8_t* stage = epi + ew * kEpiBytes;
-        int n = 0;
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+        Ring acc;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, acc.step(2)) {
             const Tile t = tile_at(seg, a, tile);
-            const int b = n & 1;
-            if (!ptx::mbar_wait(&c->acc_full[b], (n >> 1) & 1, kWaitNs)) {
+            if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
                 if (lane == 0) give_up(abort_flag);
                 *abort_flag = 1;
             }
             __syncwarp();
             if (*abort_flag) break;
             ptx::tc_fence_after();
-            const uint32_t base = tmem + b * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+            const uint32_t base = tmem + acc.s * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
             for (int tok0 = half * 32; tok0 < t.valid; tok0 += 64)
                 epilogue_chunk<MODE>(a, t, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&c->acc_empty[b]);
+            if (lane == 0) ptx::mbar_arrive(&c->acc_empty[acc.s]);
         }
     }
     __syncwarp();
@@ -627,61 +648,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t tiles = (int64_t)a.E * per_e;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int kb_all = 0;
+        if (elect_one()) {
+            Ring r;
             bool ok = true;
             for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
                 const int n0 = in / a.tiles_k * kM, k0 = in % a.tiles_k * kWN;
-                const int nkb = tiles_of(seg.count[e], kBK);
-                for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
-                    const int s = kb_all % kWStages;
-                    if (*abort_flag || !ptx::mbar_wait(&c->empty[s], ((kb_all / kWStages) & 1) ^ 1, kWaitNs)) {
+                for (int p = 0; p < seg.count[e]; p += kBK, r.step(kWStages)) {
+                    if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
-                    uint8_t* a_s = ring + s * kWStageBytes;
-                    const int row = seg.begin[e] + kb * kBK;
-                    ptx::mbar_arrive_expect_tx(&c->full[s], kWStageBytes);
+                    uint8_t* a_s = ring + r.s * kWStageBytes;
+                    const int row = seg.begin[e] + p;
+                    ptx::mbar_arrive_expect_tx(&c->full[r.s], kWStageBytes);
 #pragma unroll
                     for (int i = 0; i < kM / 64; ++i)
-                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, &c->full[s]);
+                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, &c->full[r.s]);
 #pragma unroll
                     for (int i = 0; i < kWN / 64; ++i)
-                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, &c->full[s]);
+                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, &c->full[r.s]);
                 }
             }
-            for (int k = 0; k < kWStages && k < kb_all; ++k) {
-                const int j = kb_all - 1 - k;
-                ptx::mbar_wait(&c->full[j % kWStages], (j / kWStages) & 1, kWaitNs);
-            }
+            for (int i = 0; i < kWStages; ++i, r.step(kWStages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
         const uint32_t idesc = ptx::idesc_bf16_m128(kWN, true, true);
-        int kb_all = 0, n = 0;
+        Ring r, acc;
         bool ok = true;
         for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const int e = (int)(tile / per_e);
-            const int count = seg.count[e], nkb = tiles_of(count, kBK);
-            if (nkb == 0) continue;
-            const int b = n & 1;
-            if (!ptx::mbar_wait(&c->acc_empty[b], ((n >> 1) & 1) ^ 1, kWaitNs)) {
+            const int count = seg.count[(int)(tile / per_e)];
+            if (count == 0) continue;
+            if (!ptx::mbar_wait(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
                 if (lane == 0) give_up(abort_flag);
                 break;
             }
-            ++n;
             ptx::tc_fence_after();
-            const uint32_t d = tmem + b * kAccCols;
-            for (int kb = 0; kb < nkb; ++kb, ++kb_all) {
-                const int s = kb_all % kWStages;
-                if (!ptx::mbar_wait(&c->full[s], (kb_all / kWStages) & 1, kWaitNs)) {
+            const uint32_t d = tmem + acc.s * kAccCols;
+            for (int p = 0; p < count; p += kBK, r.step(kWStages)) {
+                if (!ptx::mbar_wait(&c->full[r.s], r.phase, kWaitNs)) {
                     if (lane == 0) give_up(abort_flag);
                     ok = false;
                     break;
                 }
-                uint8_t* a_s = ring + s * kWStageBytes;
-                const int left = count - kb * kBK;           // rows of the segment in this stage
+                uint8_t* a_s = ring + r.s * kWStageBytes;
+                const int left = count - p;                                       // rows of the segment in this stage
                 const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
                 if (left < kBK) {
                     // rows [left, 16 * steps) of all six boxes are the next segment's: zero them
@@ -692,39 +704,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) {
+                if (elect_one()) {
                     ptx::tc_fence_after();
                     const uint32_t a_addr = ptx::smem_u32(a_s), b_addr = a_addr + kABytes;
-                    for (int kk = 0; kk < steps; ++kk)
-                        ptx::umma_bf16(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
-                                       ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc, (kb | kk) != 0);
-                    ptx::umma_commit(&c->empty[s]);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        if (kk < steps)
+                            ptx::umma_bf16(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
+                                           ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc, (p | kk) != 0);
+                    ptx::umma_commit(&c->empty[r.s]);
                 }
                 __syncwarp();
             }
-            if (lane == 0) ptx::umma_commit(&c->acc_full[b]);
+            if (elect_one()) ptx::umma_commit(&c->acc_full[acc.s]);
             __syncwarp();
+            acc.step(2);
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
-        int n = 0;
+        Ring acc;
         for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
             const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
             const int row = in / a.tiles_k * kM + quarter * 32 + lane, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count[e] > 0;
-            const int b = n & 1;
             if (some) {
-                if (!ptx::mbar_wait(&c->acc_full[b], (n >> 1) & 1, kWaitNs)) {
+                if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
                     if (lane == 0) give_up(abort_flag);
                     *abort_flag = 1;
                 }
-                ++n;
                 __syncwarp();
                 if (*abort_flag) break;
                 ptx::tc_fence_after();
             }
             const uint32_t base =
-                tmem + b * kAccCols + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
+                tmem + acc.s * kAccCols + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
             T* out = static_cast<T*>(a.out) + ((int64_t)e * a.N + row) * a.K + k0;
 #pragma unroll 1
             for (int j = 0; j < kWN / 2; j += 32) {
@@ -741,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (some) {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&c->acc_empty[b]);
+                if (lane == 0) ptx::mbar_arrive(&c->acc_empty[acc.s]);
+                acc.step(2);
             }
         }
     }
