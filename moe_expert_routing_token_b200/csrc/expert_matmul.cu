@@ -73,7 +73,7 @@ struct RowArgs {
     int64_t P;
     int E;
     int red;             // reduction length
-    int tiles_f;         // feature tiles
+    int tiles_f;         // pairs of feature tiles
     int tn_max;          // tokens per tile at most
     int box;             // token rows per TMA copy
     int stages, stage_bytes;
@@ -89,7 +89,7 @@ struct WeightArgs {
     const int32_t* off;
     int64_t P;
     int E, N, K;
-    int tiles_n, tiles_k;
+    int tiles_n, tiles_k;  // of 256 x 256
     void* out;
     float* grad_bias;
 };
@@ -190,15 +190,15 @@ __device__ void load_segments(Segments& s, const int32_t* off, int E, int64_t P,
 
 struct Tile {
     int e;      // expert
-    int f;      // feature tile
+    int f;      // feature tile of this CTA of the pair
     int row0;   // first token row
     int valid;  // tokens of the tile
-    int tn;     // valid rounded up to 16
+    int tn;     // valid rounded up to 32
 };
 
 // Tiles run over experts, then feature tiles, then the token tiles of the
 // expert, so that neighbouring blocks share the weight's rows.
-__device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int64_t tile) {
+__device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int64_t tile, int rank) {
     int lo = 0, hi = a.E;  // cum[lo] * tiles_f <= tile < cum[hi] * tiles_f
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -209,13 +209,14 @@ __device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int
     t.e = lo;
     const int parts = tiles_of(s.count[lo], a.tn_max);
     const int64_t in = tile - (int64_t)s.cum[lo] * a.tiles_f;
-    t.f = (int)(in / parts);
-    const int part = (int)(in - (int64_t)t.f * parts);
-    const int step = ((s.count[lo] + parts - 1) / parts + 15) & ~15;
+    const int f_pair = (int)(in / parts);
+    t.f = 2 * f_pair + rank;
+    const int part = (int)(in - (int64_t)f_pair * parts);
+    const int step = ((s.count[lo] + parts - 1) / parts + 31) & ~31;
     t.row0 = s.begin[lo] + part * step;
     const int left = s.count[lo] - part * step;
     t.valid = left < step ? left : step;
-    t.tn = (t.valid + 15) & ~15;
+    t.tn = (t.valid + 31) & ~31;
     return t;
 }
 
@@ -455,43 +456,66 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
     __syncwarp();
 }
 
-// Shared-memory layout behind the stage ring.
+// Shared-memory layout behind the stage ring.  full (the even CTA's, for
+// both): the copies of a stage have landed; tail: this CTA's copies of a stage
+// that ends a segment have, and cut (the even CTA's, for both): what they
+// brought of the next segment is zeroed; empty: a stage has been multiplied;
+// acc_full, acc_empty (the even CTA's, for both): an accumulator is complete,
+// has been read.
 struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint64_t full[kMaxStages], tail[kMaxStages], cut[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort_flag;
 };
 
+// Barriers, TMEM and the meeting of the pair's two CTAs.
 __device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             ptx::mbar_init(&c->full[s], 1);
+            ptx::mbar_init(&c->tail[s], 1);
+            ptx::mbar_init(&c->cut[s], 2);
             ptx::mbar_init(&c->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&c->acc_full[b], 1);
-            ptx::mbar_init(&c->acc_empty[b], kEpiWarps);
+            ptx::mbar_init(&c->acc_empty[b], 2 * kEpiWarps);
         }
         c->abort_flag = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 2) {
-        ptx::tmem_alloc(&c->tmem, 2 * kAccCols);
-        ptx::tmem_relinquish();
+        ptx::tmem_alloc_pair(&c->tmem, 2 * kAccCols);
+        ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
     __syncthreads();
+    ptx::cluster_sync();
     ptx::tc_fence_after();
     return c->tmem;
 }
 
+// Neither CTA of a pair leaves before the other: each reads the other's shared
+// memory and arrives on its barriers.
 __device__ __forceinline__ void end_block(uint32_t tmem, int warp) {
     ptx::tc_fence_before();
     __syncthreads();
+    ptx::cluster_sync();
     if (warp == 2) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 2 * kAccCols);
+        ptx::tmem_dealloc_pair(tmem, 2 * kAccCols);
     }
+}
+
+// Expects the copies of stage s in both CTAs (`bytes` each) on the even one's
+// barrier, whose address it gives.  Only the even CTA arrives: its barrier
+// cannot complete before, however early the other's copies land.  (An arrival
+// of the other one, a release at cluster scope, costs its producer more than a
+// stage's products: 2.90 against 1.72 ms for the first product of 4096 x 8
+// rows.)
+__device__ __forceinline__ uint32_t expect_pair(Control* c, int s, int rank, uint32_t bytes) {
+    if (rank == 0) ptx::mbar_arrive_expect_tx(&c->full[s], 2 * bytes);
+    return ptx::map_to_rank(ptx::smem_u32(&c->full[s]), 0);
 }
 
 template <int MODE>
@@ -506,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmW);
         ptx::tma_prefetch_desc(&tmX);
@@ -519,9 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             Ring r;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const Tile t = tile_at(seg, a, tile);
-                const int boxes = (t.tn + a.box - 1) / a.box;
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+                const Tile t = tile_at(seg, a, tile, rank);
+                const int row0 = t.row0 + rank * (t.tn / 2);  // this CTA's half of the tokens
+                const int boxes = (t.tn / 2 + a.box - 1) / a.box;
                 const uint32_t bytes = kABytes + boxes * a.box * kBK * 2;
                 for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
                     if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
@@ -531,8 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* a_s = ring + r.s * a.stage_bytes;
                     uint8_t* b_s = a_s + kABytes;
-                    uint64_t* full = &c->full[r.s];
-                    ptx::mbar_arrive_expect_tx(full, bytes);
+                    const uint32_t full = expect_pair(c, r.s, rank, bytes);
                     if constexpr (GRAD) {
                         ptx::tma_load(a_s, &tmW, t.f * kM, k, t.e, full);
                         ptx::tma_load(a_s + kABytes / 2, &tmW, t.f * kM + 64, k, t.e, full);
@@ -542,27 +567,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tma_load(a_s, &tmW, k, t.f * kM, t.e, full);
                     }
                     for (int i = 0; i < boxes; ++i)
-                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, k, t.row0 + i * a.box, full);
+                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, k, row0 + i * a.box, full);
                 }
             }
             // Leave only once every stage filled has been used, or its wait has run out.
             for (int i = 0; i < a.stages; ++i, r.step(a.stages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             Ring r, acc;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, acc.step(2)) {
-                const Tile t = tile_at(seg, a, tile);
-                const uint32_t idesc = ptx::idesc_bf16_m128(t.tn, GRAD, false);
-                if (!ptx::mbar_wait(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs, acc.step(2)) {
+                const Tile t = tile_at(seg, a, tile, rank);
+                const uint32_t idesc = ptx::idesc_bf16_m256(t.tn, GRAD, false);
+                if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
                     give_up(abort_flag);
                     break;
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
                 for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
-                    if (!ptx::mbar_wait(&c->full[r.s], r.phase, kWaitNs)) {
+                    if (!ptx::mbar_wait_cluster(&c->full[r.s], r.phase, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
@@ -574,19 +599,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBK / 16; ++kk) {
                         const uint64_t ad = GRAD ? ptx::sdesc_sw128(a_addr + kk * 2048, kABytes / 2, 1024)
                                                  : ptx::sdesc_sw128(a_addr + kk * 32, 16, 1024);
-                        ptx::umma_bf16(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc, (k | kk) != 0);
+                        ptx::umma_bf16_pair(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc,
+                                            (k | kk) != 0);
                     }
-                    ptx::umma_commit(&c->empty[r.s]);
+                    ptx::umma_commit_pair(&c->empty[r.s]);
                 }
-                ptx::umma_commit(&c->acc_full[acc.s]);
+                ptx::umma_commit_pair(&c->acc_full[acc.s]);
             }
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         uint8_t* stage = epi + ew * kEpiBytes;
         Ring acc;
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, acc.step(2)) {
-            const Tile t = tile_at(seg, a, tile);
+        for (int64_t tile = pair; tile < tiles; tile += pairs, acc.step(2)) {
+            const Tile t = tile_at(seg, a, tile, rank);
             if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
                 if (lane == 0) give_up(abort_flag);
                 *abort_flag = 1;
@@ -599,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 epilogue_chunk<MODE>(a, t, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&c->acc_empty[acc.s]);
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
         }
     }
     __syncwarp();
@@ -607,22 +633,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- weight gradient
-constexpr int kWN = 256;                          // columns of a tile (K side)
-constexpr int kWStages = 4;
-constexpr int kWStageBytes = kABytes + kWN * kBK * 2;
+constexpr int kWN = 256;                          // columns of a tile (K side), half in each CTA
+constexpr int kWStages = 6;
+constexpr int kWStageBytes = kABytes + kWN / 2 * kBK * 2;
 
+// Products of 16 tokens for the last `left` (or 64) of a segment.
+__device__ __forceinline__ int steps_of(int left) { return left >= kBK ? kBK / 16 : (left + 15) / 16; }
+
+// 32 values of a row whose first `cols` (a multiple of 8) exist, in accesses of
+// 32 bytes: a lane has a row to itself, so each access fills a whole sector.
 template <typename T>
 __device__ __forceinline__ void store32(T* dst, const float (&v)[32], int cols) {
-    if constexpr (sizeof(T) == 4) {
+    constexpr int N = 32 / (int)sizeof(T);
+    uint32_t w[sizeof(T) * 8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-            if (i < cols) *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
+    for (int i = 0; i < (int)sizeof(T) * 8; ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+        else w[i] = pack(v[2 * i], v[2 * i + 1]);
+    }
+    const bool wide = reinterpret_cast<uintptr_t>(dst) % 32 == 0;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            if (i < cols)
-                *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack(v[i], v[i + 1]), pack(v[i + 2], v[i + 3]),
-                                                               pack(v[i + 4], v[i + 5]), pack(v[i + 6], v[i + 7]));
+    for (int i = 0; i < 32 / N; ++i) {
+        const uint32_t* q = w + 8 * i;
+        if (wide && (i + 1) * N <= cols) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + i * N), "r"(q[0]),
+                         "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (i * N + h * (N / 2) < cols)
+                    *reinterpret_cast<uint4*>(dst + i * N + h * (N / 2)) =
+                        make_uint4(q[4 * h], q[4 * h + 1], q[4 * h + 2], q[4 * h + 3]);
+        }
     }
 }
 
@@ -637,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmY);
         ptx::tma_prefetch_desc(&tmX);
@@ -651,9 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             Ring r;
             bool ok = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                 const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
-                const int n0 = in / a.tiles_k * kM, k0 = in % a.tiles_k * kWN;
+                const int n0 = (in / a.tiles_k * 2 + rank) * kM, k0 = in % a.tiles_k * kWN + rank * (kWN / 2);
                 for (int p = 0; p < seg.count[e]; p += kBK, r.step(kWStages)) {
                     if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
@@ -662,70 +706,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* a_s = ring + r.s * kWStageBytes;
                     const int row = seg.begin[e] + p;
-                    ptx::mbar_arrive_expect_tx(&c->full[r.s], kWStageBytes);
+                    uint32_t full;
+                    if (seg.count[e] - p >= kBK) {
+                        full = expect_pair(c, r.s, rank, kWStageBytes);
+                    } else {  // warp 3 goes over this one first
+                        full = ptx::smem_u32(&c->tail[r.s]);
+                        ptx::mbar_arrive_expect_tx(&c->tail[r.s], kWStageBytes);
+                    }
 #pragma unroll
                     for (int i = 0; i < kM / 64; ++i)
-                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, &c->full[r.s]);
+                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, full);
 #pragma unroll
-                    for (int i = 0; i < kWN / 64; ++i)
-                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, &c->full[r.s]);
+                    for (int i = 0; i < kWN / 128; ++i)
+                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, full);
                 }
             }
             for (int i = 0; i < kWStages; ++i, r.step(kWStages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
-        const uint32_t idesc = ptx::idesc_bf16_m128(kWN, true, true);
-        Ring r, acc;
-        bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const int count = seg.count[(int)(tile / per_e)];
-            if (count == 0) continue;
-            if (!ptx::mbar_wait(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
-                if (lane == 0) give_up(abort_flag);
-                break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t d = tmem + acc.s * kAccCols;
-            for (int p = 0; p < count; p += kBK, r.step(kWStages)) {
-                if (!ptx::mbar_wait(&c->full[r.s], r.phase, kWaitNs)) {
-                    if (lane == 0) give_up(abort_flag);
-                    ok = false;
+        if (rank == 0 && elect_one()) {
+            const uint32_t idesc = ptx::idesc_bf16_m256(kWN, true, true);
+            Ring r, acc;
+            uint32_t uses[2] = {0, 0};  // parity of each stage's uses: whole, as a tail
+            bool ok = true;
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+                const int count = seg.count[(int)(tile / per_e)];
+                if (count == 0) continue;
+                if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
+                    give_up(abort_flag);
                     break;
                 }
-                uint8_t* a_s = ring + r.s * kWStageBytes;
-                const int left = count - p;                                       // rows of the segment in this stage
-                const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
-                if (left < kBK) {
-                    // rows [left, 16 * steps) of all six boxes are the next segment's: zero them
-                    const int pieces = (16 * steps - left) * 8;  // 16-byte pieces per box
-                    for (int i = lane; i < pieces * (kWStageBytes / 8192); i += 32)
-                        *reinterpret_cast<uint4*>(a_s + (i / pieces) * 8192 + left * 128 + (i % pieces) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    ptx::fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (elect_one()) {
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + acc.s * kAccCols;
+                for (int p = 0; p < count; p += kBK, r.step(kWStages)) {
+                    const bool whole = count - p >= kBK;
+                    uint32_t& use = uses[whole ? 0 : 1];
+                    if (!ptx::mbar_wait_cluster(whole ? &c->full[r.s] : &c->cut[r.s], use >> r.s & 1, kWaitNs)) {
+                        give_up(abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    use ^= 1u << r.s;
                     ptx::tc_fence_after();
-                    const uint32_t a_addr = ptx::smem_u32(a_s), b_addr = a_addr + kABytes;
+                    const uint32_t a_addr = ptx::smem_u32(ring + r.s * kWStageBytes), b_addr = a_addr + kABytes;
+                    const int steps = steps_of(count - p);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         if (kk < steps)
-                            ptx::umma_bf16(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
-                                           ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc, (p | kk) != 0);
-                    ptx::umma_commit(&c->empty[r.s]);
+                            ptx::umma_bf16_pair(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
+                                                ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc,
+                                                (p | kk) != 0);
+                    ptx::umma_commit_pair(&c->empty[r.s]);
                 }
-                __syncwarp();
+                ptx::umma_commit_pair(&c->acc_full[acc.s]);
+                acc.step(2);
             }
-            if (elect_one()) ptx::umma_commit(&c->acc_full[acc.s]);
+        }
+    } else if (warp == 3) {
+        // The last stage of a segment holds rows of the next one: zero them in
+        // every box, then arrive for this CTA.
+        Ring r;
+        uint32_t uses = 0;  // parity of each stage's uses as a tail
+        bool ok = true;
+        for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+            const int count = seg.count[(int)(tile / per_e)], left = count % kBK;
+            for (int p = kBK; p <= count; p += kBK) r.step(kWStages);
+            if (left == 0) continue;
+            if (!ptx::mbar_wait(&c->tail[r.s], uses >> r.s & 1, kWaitNs)) {
+                if (lane == 0) give_up(abort_flag);
+                ok = false;
+                break;
+            }
+            uses ^= 1u << r.s;
+            uint8_t* a_s = ring + r.s * kWStageBytes;
+            const int pieces = (16 * steps_of(left) - left) * 8;  // 16-byte pieces per 64-column box
+            for (int i = lane; i < pieces * (kWStageBytes / 8192); i += 32)
+                *reinterpret_cast<uint4*>(a_s + (i / pieces) * 8192 + left * 128 + (i % pieces) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();
             __syncwarp();
-            acc.step(2);
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->cut[r.s]), 0));
+            r.step(kWStages);
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         Ring acc;
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (int64_t tile = pair; tile < tiles; tile += pairs) {
             const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
-            const int row = in / a.tiles_k * kM + quarter * 32 + lane, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
+            const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32 + lane, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count[e] > 0;
             if (some) {
                 if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
@@ -754,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (some) {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&c->acc_empty[acc.s]);
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
                 acc.step(2);
             }
         }
@@ -849,17 +917,21 @@ int allow_smem(const void* kern, int dev, size_t bytes) {
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, const char* who, void* stream, Args... args) {
+int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t smem, const char* who, void* stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t err = cudaLaunchKernelEx(&cfg, kern, args...);
     return err == cudaSuccess ? MOE_OK : set_cuda_error(err, who);
 }
@@ -868,15 +940,15 @@ constexpr size_t kSmemMax = 232448;  // 227 KB
 constexpr size_t kTail = kEpiWarps * kEpiBytes + sizeof(Control) + sizeof(Segments);
 constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + sizeof(Control) + sizeof(Segments);
 static_assert(kWeightSmem <= kSmemMax, "weight gradient's shared memory");
-static_assert(1024 + 4 * (kABytes + 256 * kBK * 2) + kTail <= kSmemMax, "row products' shared memory");
+static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + kTail <= kSmemMax, "row products' shared memory");
 
 // Tokens per tile, by the experts' mean share of rows: narrow tiles leave
 // room for more stages, which a product that waits for its weights needs.
 void choose_tile(RowArgs& a) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
-    a.box = a.tn_max <= 64 ? 16 : a.tn_max / 4;
-    a.stage_bytes = kABytes + a.tn_max * kBK * 2;
+    a.box = a.tn_max <= 64 ? 16 : 32;
+    a.stage_bytes = kABytes + a.tn_max / 2 * kBK * 2;
     const int fit = (int)((kSmemMax - 1024 - kTail) / a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
 }
@@ -892,7 +964,7 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, a.box);
     if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kTail;
-    return launch(expert_rows_kernel<MODE>, dim3(sms), kThreads, smem, who, stream, tmW, tmX, a);
+    return launch(expert_rows_kernel<MODE>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmW, tmX, a);
 }
 
 bool bad(const void* p, size_t n) { return !p || reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -959,7 +1031,7 @@ int moe_expert_matmul(const void* x, const void* weight, const int32_t* expert_o
     a.E = E;
     a.red = K;
     a.N = N;
-    a.tiles_f = gated ? (N + 63) / 64 : (N + kM - 1) / kM;
+    a.tiles_f = gated ? (N + kM - 1) / kM : (N + 2 * kM - 1) / (2 * kM);
     a.bias = bias;
     a.act = activation;
     a.extra = (const bf16*)residual;
@@ -1001,7 +1073,7 @@ int moe_expert_matmul_grad_input(const void* grad_out, const void* weight, const
     a.E = E;
     a.red = N;
     a.N = K;
-    a.tiles_f = (K + kM - 1) / kM;
+    a.tiles_f = (K + 2 * kM - 1) / (2 * kM);
     a.act = activation;
     a.extra = (const bf16*)preact;
     a.out = (bf16*)grad_x;
@@ -1031,7 +1103,7 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     int dev = 0, sms = 0;
     int rc2 = sm_count(&dev, &sms);
     if (rc2 != MOE_OK) return rc2;
-    WeightArgs a = {expert_offsets, P, E, N, K, (N + kM - 1) / kM, (K + kWN - 1) / kWN, grad_weight, grad_bias};
+    WeightArgs a = {expert_offsets, P, E, N, K, (N + 2 * kM - 1) / (2 * kM), (K + kWN - 1) / kWN, grad_weight, grad_bias};
     CUtensorMap tmY, tmX;
     // with P == 0 nothing is read through the maps; they still have to be valid ones
     cudaError_t err = encode_rows(&tmY, P ? grad_out : grad_weight, P ? P : 1, N, kBK);
@@ -1040,14 +1112,14 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     if (dtype == MOE_DTYPE_F32) {
         rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kWeightSmem);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<float>, dim3(sms), kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, a);
     } else {
         rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kWeightSmem);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms), kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, a);
     }
     if (rc2 != MOE_OK || !grad_bias) return rc2;
-    return launch(expert_bias_kernel, dim3((N + 255) / 256, E), 256, 0, who, stream, (const bf16*)grad_out,
+    return launch(expert_bias_kernel, dim3((N + 255) / 256, E), 1, 256, 0, who, stream, (const bf16*)grad_out,
                   expert_offsets, P, (int)N, grad_bias);
 }
 
