@@ -54,12 +54,24 @@ template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Places of up to 32 slots from j0 on: lane j holds slot j0 + j's, 0xffffffff
+// if it has none; the return value has a bit for each slot that has.
+__device__ __forceinline__ uint32_t places(const int32_t* scatter, int64_t t, int k, int j0, uint32_t P, int lane,
+                                           uint32_t* place) {
+    *place = j0 + lane < k ? (uint32_t)__ldg(scatter + t * k + j0 + lane) : 0xffffffffu;
+    return __ballot_sync(0xffffffffu, *place < P);
+}
+
+// Accesses a lane has in flight per row: 64 bytes, at most 8 accesses.
+template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : 8; }
+
 // One warp per (token, segment of 32 * U accesses of the row).
-template <typename T, int VB, int U>
+template <typename T, int VB>
 __global__ void __launch_bounds__(kTokThreads)
     gather_kernel(const T* x, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
                   T* sorted, int segs) {
     using C = Chunk<T, VB>;
+    constexpr int U = unroll<VB>();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
     ptx::griddep_wait();
@@ -68,26 +80,35 @@ __global__ void __launch_bounds__(kTokThreads)
     const int64_t c0 = (item % segs) * (32 * U) + lane;  // this lane's first access in the row
     const int64_t n = H / C::N;
     typename C::V v[U];
+    bool loaded = false;
     const auto* src = reinterpret_cast<const typename C::V*>(x + t * H);
+    for (int j0 = 0; j0 < k; j0 += 32) {
+        uint32_t place;
+        uint32_t todo = places(scatter, t, k, j0, P, lane, &place);
+        if (todo && !loaded) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (c0 + 32 * u < n) v[u] = src[c0 + 32 * u];
-    for (int j = 0; j < k; ++j) {
-        const uint32_t p = (uint32_t)__ldg(scatter + t * k + j);
-        if (p >= P) continue;
-        auto* dst = reinterpret_cast<typename C::V*>(sorted + (int64_t)p * H);
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < n) v[u] = src[c0 + 32 * u];
+            loaded = true;
+        }
+        for (; todo; todo &= todo - 1) {
+            const uint32_t p = __shfl_sync(0xffffffffu, place, __ffs(todo) - 1);
+            auto* dst = reinterpret_cast<typename C::V*>(sorted + (int64_t)p * H);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + 32 * u < n) dst[c0 + 32 * u] = v[u];
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < n) dst[c0 + 32 * u] = v[u];
+        }
     }
 }
 
-// One warp per (token, segment): the weighted sum of the token's rows.
-template <typename T, int VB, int U, bool WEIGHTED>
+// One warp per (token, segment): the weighted sum of the token's rows, R of
+// them in flight at a time.
+template <typename T, int VB, bool WEIGHTED>
 __global__ void __launch_bounds__(kTokThreads)
     combine_kernel(const T* y, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
                    const float* __restrict__ weights, const T* residual, T* out, int segs) {
     using C = Chunk<T, VB>;
+    constexpr int U = unroll<VB>() / 2, R = 4;
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
     ptx::griddep_wait();
@@ -100,92 +121,114 @@ __global__ void __launch_bounds__(kTokThreads)
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < C::N; ++i) acc[u][i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const uint32_t p = (uint32_t)__ldg(scatter + t * k + j);
-        if (p >= P) continue;
-        const float w = WEIGHTED ? __ldg(weights + t * k + j) : 1.0f;
-        const auto* src = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H);
+    C r[U];
+    if (residual != nullptr) {
+        const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (c0 + 32 * u >= n) continue;
-            C c;
-            c.v = src[c0 + 32 * u];
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < n) r[u].v = res[c0 + 32 * u];
+    }
+    for (int j0 = 0; j0 < k; j0 += 32) {
+        uint32_t place;
+        uint32_t todo = places(scatter, t, k, j0, P, lane, &place);
+        const float weight = WEIGHTED && j0 + lane < k ? __ldg(weights + t * k + j0 + lane) : 1.0f;
+        while (todo) {
+            C c[R][U];
+            float w[R];
+            const int rows = min(__popc(todo), R);
 #pragma unroll
-            for (int i = 0; i < C::N; ++i)
-                acc[u][i] = WEIGHTED ? fmaf(w, to_f32(c.t[i]), acc[u][i]) : acc[u][i] + to_f32(c.t[i]);
+            for (int q = 0; q < R; ++q) {
+                if (q >= rows) break;
+                const int j = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const uint32_t p = __shfl_sync(0xffffffffu, place, j);
+                w[q] = WEIGHTED ? __shfl_sync(0xffffffffu, weight, j) : 1.0f;
+                const auto* src = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < n) c[q][u].v = src[c0 + 32 * u];
+            }
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (q >= rows) break;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < n)
+#pragma unroll
+                        for (int i = 0; i < C::N; ++i)
+                            acc[u][i] = WEIGHTED ? fmaf(w[q], to_f32(c[q][u].t[i]), acc[u][i])
+                                                 : acc[u][i] + to_f32(c[q][u].t[i]);
+            }
         }
     }
-    const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H);
     auto* dst = reinterpret_cast<typename C::V*>(out + t * H);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (c0 + 32 * u >= n) continue;
         C c;
-        if (residual != nullptr) {
-            c.v = res[c0 + 32 * u];
 #pragma unroll
-            for (int i = 0; i < C::N; ++i) acc[u][i] += to_f32(c.t[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < C::N; ++i) c.t[i] = from_f32<T>(acc[u][i]);
+        for (int i = 0; i < C::N; ++i)
+            c.t[i] = from_f32<T>(residual != nullptr ? acc[u][i] + to_f32(r[u].t[i]) : acc[u][i]);
         dst[c0 + 32 * u] = c.v;
     }
 }
 
-// One block per token; KB slots a pass, their dot products in registers and
-// then summed over the block in a fixed order.
-constexpr int KB = 8;
-template <typename T, int VB>
-__global__ void __launch_bounds__(kTokThreads)
-    combine_backward_kernel(const T* grad_out, const T* y, int64_t H, const int32_t* __restrict__ scatter, int k,
-                            uint32_t P, const float* __restrict__ weights, T* grad_y, float* grad_weights) {
+// W warps per (token, slot): a row of grad_y and one dot product.  The token's
+// row of grad_out comes from cache for all but its first slot.
+template <typename T, int VB, int W>
+__global__ void __launch_bounds__(256)
+    combine_backward_kernel(const T* grad_out, const T* y, int64_t pairs, int64_t H,
+                            const int32_t* __restrict__ scatter, int k, const float* __restrict__ weights, T* grad_y,
+                            float* grad_weights) {
     using C = Chunk<T, VB>;
-    __shared__ float s_dot[kTokWarps][KB];
-    const int64_t t = blockIdx.x;
+    constexpr int U = unroll<VB>();
+    __shared__ float s_dot[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = H / C::N;
+    const int64_t i = (int64_t)blockIdx.x * (8 / W) + warp / W;
     ptx::griddep_wait();
-    const auto* g_row = reinterpret_cast<const typename C::V*>(grad_out + t * H);
-    for (int j0 = 0; j0 < k; j0 += KB) {
-        uint32_t p[KB];
-        float w[KB], dot[KB];
+    float dot = 0.0f;
+    if (i < pairs) {
+        const uint32_t p = (uint32_t)__ldg(scatter + i);
+        if (p < pairs) {
+            const float w = __ldg(weights + i);
+            const int64_t n = H / C::N;
+            const auto* g_row = reinterpret_cast<const typename C::V*>(grad_out + i / k * H);
+            const auto* y_row = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H);
+            auto* d_row = reinterpret_cast<typename C::V*>(grad_y + (int64_t)p * H);
+            for (int64_t c0 = (warp % W) * 32 + lane; c0 < n; c0 += 32 * W * U) {
+                C g[U], v[U];
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            p[j] = j0 + j < k ? (uint32_t)__ldg(scatter + t * k + j0 + j) : 0xffffffffu;
-            w[j] = p[j] < P ? __ldg(weights + t * k + j0 + j) : 0.0f;
-            dot[j] = 0.0f;
-        }
-        for (int64_t c = threadIdx.x; c < n; c += kTokThreads) {
-            C g;
-            g.v = g_row[c];
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * W * u < n) {
+                        g[u].v = g_row[c0 + 32 * W * u];
+                        v[u].v = y_row[c0 + 32 * W * u];
+                    }
 #pragma unroll
-            for (int j = 0; j < KB; ++j) {
-                if (p[j] >= P) continue;
-                C v, d;
-                v.v = reinterpret_cast<const typename C::V*>(y + (int64_t)p[j] * H)[c];
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * W * u < n) {
+                        C d;
 #pragma unroll
-                for (int i = 0; i < C::N; ++i) {
-                    dot[j] = fmaf(to_f32(g.t[i]), to_f32(v.t[i]), dot[j]);
-                    d.t[i] = from_f32<T>(w[j] * to_f32(g.t[i]));
-                }
-                reinterpret_cast<typename C::V*>(grad_y + (int64_t)p[j] * H)[c] = d.v;
+                        for (int e = 0; e < C::N; ++e) {
+                            dot = fmaf(to_f32(g[u].t[e]), to_f32(v[u].t[e]), dot);
+                            d.t[e] = from_f32<T>(w * to_f32(g[u].t[e]));
+                        }
+                        d_row[c0 + 32 * W * u] = d.v;
+                    }
             }
         }
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-        if (lane == 0)
-#pragma unroll
-            for (int j = 0; j < KB; ++j) s_dot[warp][j] = dot[j];
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (W == 1 && lane == 0) grad_weights[i] = dot;
+    }
+    if constexpr (W > 1) {  // W = 8: the block's one pair
+        if (lane == 0) s_dot[warp] = dot;
         __syncthreads();
-        if (threadIdx.x < KB && j0 + (int)threadIdx.x < k) {
+        if (threadIdx.x == 0) {
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kTokWarps; ++i) s += s_dot[i][threadIdx.x];
-            grad_weights[t * k + j0 + threadIdx.x] = s;
+            for (int w = 0; w < 8; ++w) s += s_dot[w];
+            grad_weights[i] = s;
         }
-        __syncthreads();
     }
 }
 
@@ -201,10 +244,10 @@ int access_bytes(int64_t H, const void* a, const void* b, const void* c = nullpt
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), int64_t blocks, const char* who, void* stream, Args... args) {
+int launch(void (*kern)(KArgs...), int64_t blocks, int threads, const char* who, void* stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3(kTokThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -254,34 +297,36 @@ int check(const TokArgs& a, int dtype, std::initializer_list<const void*> rows, 
     return MOE_OK;
 }
 
-// Accesses in flight per lane and row segment.
-constexpr int kUnroll = 4;
-
 template <typename T, int VB>
 int run_gather(const TokArgs& a, const void* x, void* sorted) {
-    const int64_t n = a.H / (VB / (int)sizeof(T));
-    const int segs = (int)((n + 32 * kUnroll - 1) / (32 * kUnroll));
+    const int64_t n = a.H / (VB / (int)sizeof(T)), per = 32 * unroll<VB>();
+    const int segs = (int)((n + per - 1) / per);
     const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
     if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_gather_tokens: M*H needs too many blocks");
-    return launch(gather_kernel<T, VB, kUnroll>, blocks, a.who, a.stream, (const T*)x, a.M, a.H, a.scatter, a.k,
+    return launch(gather_kernel<T, VB>, blocks, kTokThreads, a.who, a.stream, (const T*)x, a.M, a.H, a.scatter, a.k,
                   (uint32_t)(a.M * a.k), (T*)sorted, segs);
 }
 
 template <typename T, int VB, bool WEIGHTED>
 int run_combine(const TokArgs& a, const void* y, const float* w, const void* residual, void* out) {
-    constexpr int U = 2;
-    const int64_t n = a.H / (VB / (int)sizeof(T));
-    const int segs = (int)((n + 32 * U - 1) / (32 * U));
+    const int64_t n = a.H / (VB / (int)sizeof(T)), per = 32 * (unroll<VB>() / 2);
+    const int segs = (int)((n + per - 1) / per);
     const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
     if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_combine_tokens: M*H needs too many blocks");
-    return launch(combine_kernel<T, VB, U, WEIGHTED>, blocks, a.who, a.stream, (const T*)y, a.M, a.H, a.scatter, a.k,
-                  (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, segs);
+    return launch(combine_kernel<T, VB, WEIGHTED>, blocks, kTokThreads, a.who, a.stream, (const T*)y, a.M, a.H,
+                  a.scatter, a.k, (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, segs);
 }
+
+// A warp per pair from this many pairs on, a block per pair below.
+constexpr int64_t kWarpPairs = 4096;
 
 template <typename T, int VB>
 int run_combine_backward(const TokArgs& a, const void* g, const void* y, const float* w, void* gy, float* gw) {
-    return launch(combine_backward_kernel<T, VB>, a.M, a.who, a.stream, (const T*)g, (const T*)y, a.H, a.scatter, a.k,
-                  (uint32_t)(a.M * a.k), w, (T*)gy, gw);
+    const int64_t pairs = a.M * a.k;
+    const bool warps = pairs >= kWarpPairs;
+    return launch(warps ? combine_backward_kernel<T, VB, 1> : combine_backward_kernel<T, VB, 8>,
+                  warps ? (pairs + 7) / 8 : pairs, 256, a.who, a.stream, (const T*)g, (const T*)y, pairs, a.H,
+                  a.scatter, a.k, w, (T*)gy, gw);
 }
 
 // F<T, VB>(args...) for the row type and access width.

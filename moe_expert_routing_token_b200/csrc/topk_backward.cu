@@ -9,10 +9,13 @@
 //   sigmoid, renorm    S = sum_l p_l: dz_j = (g_j - sum_l g_l p_l / S) / S * p_j (1 - p_j)
 //   softcap            dx = dz (1 - tanh(x / softcap)^2)
 //
-// One warp per row, lane j holds slot j (k <= 32); the row of the gradient is
-// put together in shared memory and stored whole.  Reads k logits a row (the
-// whole row only for the softmax without renormalisation) and writes M * E
-// values: bound by HBM writes for large batches, by launch latency below.
+// Lane j of a group of L lanes (8, 16 or 32, as k needs) holds slot j of a row.
+// The row of the gradient is filled first, with zeros or, for the softmax
+// without renormalisation, with -p_e sum_l g_l p_l from registers; then each
+// slot's lane stores its own element over it (the warp's barrier between
+// orders the two).  Reads k logits a row (the whole row only for the softmax
+// without renormalisation) and writes M * E values: HBM writes bound large
+// batches, launch latency the small ones.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -47,93 +50,178 @@ __device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
+__device__ __forceinline__ float cap(float x, float c) { return c != 0.0f ? c * tanhf(x / c) : x; }
+// d cap / d x
+__device__ __forceinline__ float cap_slope(float x, float c) {
+    if (c == 0.0f) return 1.0f;
+    const float h = tanhf(x / c);
+    return 1.0f - h * h;
+}
+
+// Sum over the slots of this group that share this lane's expert, and whether
+// this lane is the first of them.
+template <int L>
+__device__ __forceinline__ float joint(float v, int id, bool mine, int k, bool* first) {
+    const int lane = threadIdx.x & 31, g0 = lane & ~(L - 1);
+    float sum = 0.0f;
+    *first = mine;
+    for (int j = 0; j < k; ++j) {
+        const float t = __shfl_sync(0xffffffffu, v, g0 + j);
+        const int i = __shfl_sync(0xffffffffu, mine ? id : -1, g0 + j);
+        if (mine && i == id) {
+            sum += t;
+            if (g0 + j < lane) *first = false;
+        }
+    }
+    return sum;
+}
+
+// Everything but the dense softmax: nothing outside the chosen experts.
+template <typename T, int L>
+__global__ void __launch_bounds__(kGradWarps * 32) chosen_kernel(GradArgs a, int wide) {
+    const int lane = threadIdx.x & 31, slot = lane % L;
+    const int64_t row = ((int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5)) * (32 / L) + lane / L;
+    ptx::griddep_wait();
+    const bool live = row < a.M;
+    const T* x = static_cast<const T*>(a.logits) + row * a.E;
+    T* out = static_cast<T*>(a.out) + row * a.E;
+
+    const int id = live && slot < a.k ? __ldg(a.ids + row * a.k + slot) : -1;
+    const bool mine = (uint32_t)id < (uint32_t)a.E;
+    const float g = mine ? a.rsf * __ldg(a.grad + row * a.k + slot) : 0.0f;
+    const float raw = mine ? load_f32(x + id) : 0.0f;
+    if (live) {
+        if (wide) {  // rows of whole 16-byte pieces
+            const int n = a.E * (int)sizeof(T) / 16;
+            for (int c = slot; c < n; c += L) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int e = slot; e < a.E; e += L) put(out + e, 0.0f);
+        }
+    }
+    float v;
+    if (a.scoring == MOE_SCORE_SOFTMAX) {
+        const float z = cap(raw, a.softcap);
+        const float m = group_max<L>(mine ? z : -INFINITY);
+        float p = mine ? expf(z - m) : 0.0f;
+        const float s = group_sum<L>(p);
+        p = mine ? p / s : 0.0f;
+        const float mean = group_sum<L>(g * p);
+        v = p * (g - mean) * cap_slope(raw, a.softcap);
+    } else {
+        const float p = mine ? 1.0f / (1.0f + expf(-raw)) : 0.0f;
+        const float q = mine ? 1.0f / (1.0f + expf(raw)) : 0.0f;  // 1 - p without cancellation
+        v = g * p * q;
+        if (a.renorm) {
+            const float s = group_sum<L>(p);
+            const float mean = group_sum<L>(g * p);
+            v = mine ? (g - mean / s) / s * p * q : 0.0f;
+        }
+    }
+    bool first;
+    const float sum = joint<L>(v, id, mine, a.k, &first);
+    __syncwarp();
+    if (first) put(out + id, sum);
+}
+
+// The softmax without renormalisation: every expert of the row takes part.
+// One warp per row, the row's values in registers (up to 1024 experts).
 template <typename T>
-__global__ void __launch_bounds__(kGradWarps * 32) topk_backward_kernel(GradArgs a) {
-    extern __shared__ float s_rows[];
+__global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int wide) {
+    constexpr int N = 16 / (int)sizeof(T);  // values of a 16-byte piece
+    constexpr int PIECES = 1024 / 32 / N;
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
     ptx::griddep_wait();
     if (row >= a.M) return;
     const T* x = static_cast<const T*>(a.logits) + row * a.E;
-    float* dz = s_rows + (threadIdx.x >> 5) * a.E;
-    const bool capped = a.softcap != 0.0f;
+    T* out = static_cast<T*>(a.out) + row * a.E;
 
-    int id = lane < a.k ? __ldg(a.ids + row * a.k + lane) : -1;
+    const int id = lane < a.k ? __ldg(a.ids + row * a.k + lane) : -1;
     const bool mine = (uint32_t)id < (uint32_t)a.E;
     const float g = mine ? a.rsf * __ldg(a.grad + row * a.k + lane) : 0.0f;
-    float z = mine ? load_f32(x + id) : 0.0f;
-    if (capped) z = a.softcap * tanhf(z / a.softcap);
+    const float raw = mine ? load_f32(x + id) : 0.0f;
 
-    float v;            // this slot's dz
-    float rest = 0.0f;  // softmax without renormalisation: sum_l g_l p_l
-    float top = 0.0f, total = 1.0f;
-    const bool dense = a.scoring == MOE_SCORE_SOFTMAX && !a.renorm;
-    if (dense) {
-        top = -INFINITY;
-        for (int e = lane; e < a.E; e += 32) {
-            float t = load_f32(x + e);
-            if (capped) t = a.softcap * tanhf(t / a.softcap);
-            dz[e] = t;
+    // values e = (lane + 32 i) * N + u, -inf past the row
+    float z[PIECES][N];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int e0 = (lane + 32 * i) * N;
+        union {
+            uint4 v;
+            T t[N];
+        } c;
+        if (wide && e0 < a.E) c.v = *reinterpret_cast<const uint4*>(x + e0);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            float t = -INFINITY;
+            if (e0 + u < a.E) t = cap(wide ? (float)c.t[u] : load_f32(x + e0 + u), a.softcap);
+            z[i][u] = t;
             top = fmaxf(top, t);
         }
-        top = warp_max(top);
-        float s = 0.0f;
-        for (int e = lane; e < a.E; e += 32) s += expf(dz[e] - top);
-        total = warp_sum(s);
-        const float p = mine ? expf(z - top) / total : 0.0f;
-        rest = warp_sum(g * p);
-        v = g * p;
-    } else if (a.scoring == MOE_SCORE_SOFTMAX) {
-        const float m = warp_max(mine ? z : -INFINITY);
-        float p = mine ? expf(z - m) : 0.0f;
-        const float s = warp_sum(p);
-        p = mine ? p / s : 0.0f;
-        v = p * (g - warp_sum(g * p));
-    } else {
-        const float p = mine ? 1.0f / (1.0f + expf(-z)) : 0.0f;
-        const float q = mine ? 1.0f / (1.0f + expf(z)) : 0.0f;  // 1 - p without cancellation
-        if (a.renorm) {
-            const float s = warp_sum(p);
-            const float mean = warp_sum(g * p);
-            v = mine ? (g - mean / s) / s * p * q : 0.0f;
+    }
+    top = group_max<32>(top);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        if (i * 32 * N >= a.E) break;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            z[i][u] = expf(z[i][u] - top);
+            s += z[i][u];
+        }
+    }
+    const float total = group_sum<32>(s);
+    const float p = mine ? expf(cap(raw, a.softcap) - top) / total : 0.0f;
+    const float rest = group_sum<32>(g * p);
+    bool first;
+    const float sum = joint<32>(g * p, id, mine, a.k, &first);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int e0 = (lane + 32 * i) * N;
+        if (e0 >= a.E) break;
+        union {
+            uint4 v;
+            T t[N];
+        } c;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            float t = -rest * (z[i][u] / total);
+            if (a.softcap != 0.0f && e0 + u < a.E) t *= cap_slope(load_f32(x + e0 + u), a.softcap);
+            put(&c.t[u], t);
+        }
+        if (wide) {
+            *reinterpret_cast<uint4*>(out + e0) = c.v;
         } else {
-            v = g * p * q;
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (e0 + u < a.E) out[e0 + u] = c.t[u];
         }
     }
-    // an expert chosen twice gets both slots' share, from the first of them
-    const unsigned same = __match_any_sync(0xffffffffu, mine ? id : -1 - lane);
-    float sum = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        const float t = __shfl_sync(0xffffffffu, v, j);
-        if (same >> j & 1) sum += t;
-    }
-    const bool first = mine && (__ffs(same) - 1 == lane);
+    __syncwarp();
+    if (first) put(out + id, (sum - rest * p) * cap_slope(raw, a.softcap));
+}
 
-    __syncwarp();
-    for (int e = lane; e < a.E; e += 32) dz[e] = dense ? -rest * (expf(dz[e] - top) / total) : 0.0f;
-    __syncwarp();
-    if (first) dz[id] += sum;
-    __syncwarp();
-    T* out = static_cast<T*>(a.out) + row * a.E;
-    for (int e = lane; e < a.E; e += 32) {
-        float t = dz[e];
-        if (capped) {
-            const float h = tanhf(load_f32(x + e) / a.softcap);
-            t *= 1.0f - h * h;
-        }
-        put(out + e, t);
-    }
+template <typename T>
+void (*pick(const GradArgs& a, int* rows_per_warp))(GradArgs, int) {
+    *rows_per_warp = 1;
+    if (a.scoring == MOE_SCORE_SOFTMAX && !a.renorm) return dense_kernel<T>;
+    if (a.k > 16) return chosen_kernel<T, 32>;
+    *rows_per_warp = a.k > 8 ? 2 : 4;
+    return a.k > 8 ? chosen_kernel<T, 16> : chosen_kernel<T, 8>;
 }
 
 }  // namespace
@@ -170,17 +258,19 @@ extern "C" int moe_topk_backward(const float* grad_weights, const void* gating_o
 
     GradArgs a{grad_weights, gating_output, topk_ids, grad_logits, M, E, k, scoring, renormalize ? 1 : 0,
                routed_scaling_factor, softcap};
+    int rows = 1;
+    auto kern = dtype == MOE_DTYPE_F32 ? pick<float>(a, &rows) : pick<__nv_bfloat16>(a, &rows);
+    const int wide = (size_t)E * esz % 16 == 0 && !bad(gating_output, 16) && !bad(grad_logits, 16);
+    rows *= kGradWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((M + kGradWarps - 1) / kGradWarps), 1, 1);
+    cfg.gridDim = dim3((unsigned)((M + rows - 1) / rows), 1, 1);
     cfg.blockDim = dim3(kGradWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)kGradWarps * E * 4;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t err = dtype == MOE_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, topk_backward_kernel<float>, a)
-                                             : cudaLaunchKernelEx(&cfg, topk_backward_kernel<__nv_bfloat16>, a);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, wide);
     return err == cudaSuccess ? MOE_OK : set_cuda_error(err, "moe_topk_backward launch");
 }

@@ -31,30 +31,32 @@ from __future__ import annotations
 import torch
 
 from .routing import (MOE_ACT_GELU, MOE_ACT_NONE, MOE_ACT_SILU, MOE_OK, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, _check,
-                      _cuda_2d, _dtype_code, _on, _same_device, lib)
+                      _cuda_2d, _dtype_code, _on, lib)
 
 ACTIVATIONS = {"none": MOE_ACT_NONE, "silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
 SCORINGS = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 
 def _activation(name: str) -> int:
-    if name not in ACTIVATIONS:
+    code = ACTIVATIONS.get(name)
+    if code is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {name!r}")
-    return ACTIVATIONS[name]
+    return code
 
 
-def _call(name: str, device, *args) -> None:
-    """The C entry point ``name`` on ``device``'s current stream.  The raw
-    handle is torch.cuda.current_stream(device).cuda_stream without the Python
-    object around it, and the device is switched only where it has to be: a
-    small call's time is the host's (one call of a small batch takes 6 to 8 us
-    with both, 11 to 14 without; its kernel 3 to 4)."""
+def _call(name: str, index: int, *args) -> None:
+    """The C entry point ``name`` on the current stream of device ``index``.
+
+    A small call's time is the host's: the raw handle is
+    torch.cuda.current_stream(index).cuda_stream without the Python object
+    around it, the device is switched only where it has to be, and devices are
+    compared by number."""
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with _on(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        with _on(torch.device("cuda", index)):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != MOE_OK:
         _check(st, name)
 
@@ -63,19 +65,27 @@ def _like(t, name: str, like: torch.Tensor, shape, dtype) -> torch.Tensor:
     """The given tensor, checked, or a new one on ``like``'s device."""
     if t is None:
         return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
-    _expect(t, name, shape, dtype, like.device)
+    _expect(t, name, shape, dtype, like.get_device())
     return t
 
 
-def _expect(t: torch.Tensor, name: str, shape, dtype, device) -> None:
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+def _expect(t: torch.Tensor, name: str, shape, dtype, index: int) -> None:
+    if not (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on cuda:{index}")
 
 
-def _scatter(scatter_indx: torch.Tensor, pairs: int, device) -> None:
-    if scatter_indx.dtype != torch.int32 or scatter_indx.numel() != pairs or not scatter_indx.is_contiguous() or \
-            scatter_indx.device != device:
-        raise ValueError(f"scatter_indx must be a contiguous int32 tensor of {pairs} places on {device}")
+def _rows(t: torch.Tensor, name: str) -> int:
+    """A contiguous 2-D CUDA tensor's device number."""
+    index = t.get_device()
+    if index < 0 or t.dim() != 2 or not t.is_contiguous():
+        _cuda_2d(t, name)
+    return index
+
+
+def _scatter(scatter_indx: torch.Tensor, pairs: int, index: int) -> None:
+    if not (scatter_indx.dtype is torch.int32 and scatter_indx.numel() == pairs and scatter_indx.is_contiguous()
+            and scatter_indx.get_device() == index):
+        raise ValueError(f"scatter_indx must be a contiguous int32 tensor of {pairs} places on cuda:{index}")
 
 
 def _tokens_of(rows: torch.Tensor, k: int, name: str) -> int:
@@ -84,31 +94,26 @@ def _tokens_of(rows: torch.Tensor, k: int, name: str) -> int:
     return rows.shape[0] // k
 
 
-def _bf16(t: torch.Tensor, name: str) -> None:
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be bfloat16")
-
-
 def gather_tokens(x: torch.Tensor, scatter_indx: torch.Tensor, topk: int, out=None) -> torch.Tensor:
     """Token rows (M, H) to their places in expert order: (M * topk, H), by the
     scatter indices of ``expert_permutation`` (moe_gather_tokens)."""
-    _cuda_2d(x, "x")
+    dev = _rows(x, "x")
     M, H = x.shape
     topk = int(topk)
     code = _dtype_code(x)
     if topk < 1:
         raise ValueError("topk must be positive")
-    _scatter(scatter_indx, M * topk, x.device)
+    _scatter(scatter_indx, M * topk, dev)
     out = _like(out, "out", x, (M * topk, H), x.dtype)
-    _call("moe_gather_tokens", x.device, x.data_ptr(), code, M, H, scatter_indx.data_ptr(), topk, out.data_ptr())
+    _call("moe_gather_tokens", dev, x.data_ptr(), code, M, H, scatter_indx.data_ptr(), topk, out.data_ptr())
     return out
 
 
 def gather_tokens_backward(grad_sorted: torch.Tensor, scatter_indx: torch.Tensor, topk: int, out=None) -> torch.Tensor:
     """Gradient of ``gather_tokens``: (M * topk, H) to (M, H), each token the
     sum of its places' rows (moe_gather_tokens_backward)."""
-    _cuda_2d(grad_sorted, "grad_sorted")
-    dev, H, topk = grad_sorted.device, grad_sorted.shape[1], int(topk)
+    dev = _rows(grad_sorted, "grad_sorted")
+    H, topk = grad_sorted.shape[1], int(topk)
     code = _dtype_code(grad_sorted)
     M = _tokens_of(grad_sorted, topk, "grad_sorted")
     _scatter(scatter_indx, M * topk, dev)
@@ -118,22 +123,18 @@ def gather_tokens_backward(grad_sorted: torch.Tensor, scatter_indx: torch.Tensor
     return out
 
 
-def _weights(topk_weights: torch.Tensor):
-    _cuda_2d(topk_weights, "topk_weights")
-    if topk_weights.dtype != torch.float32:
-        raise ValueError("topk_weights must be float32")
-    return topk_weights.shape
-
-
 def combine_tokens(y: torch.Tensor, scatter_indx: torch.Tensor, topk_weights: torch.Tensor, residual=None,
                    out=None) -> torch.Tensor:
     """The experts' rows (M * k, H) back to their tokens, weighted and summed,
     plus ``residual`` (M, H): (M, H) of y's dtype (moe_combine_tokens)."""
-    _cuda_2d(y, "y")
-    M, k = _weights(topk_weights)
-    dev, H = y.device, y.shape[1]
+    dev = _rows(y, "y")
+    _rows(topk_weights, "topk_weights")
+    M, k = topk_weights.shape
+    H = y.shape[1]
     code = _dtype_code(y)
-    _expect(y, "y", (M * k, H), y.dtype, topk_weights.device)
+    _expect(topk_weights, "topk_weights", (M, k), torch.float32, dev)
+    if y.shape[0] != M * k:
+        raise ValueError(f"y must have a row for each of the {M * k} places")
     _scatter(scatter_indx, M * k, dev)
     if residual is not None:
         _expect(residual, "residual", (M, H), y.dtype, dev)
@@ -148,11 +149,14 @@ def combine_tokens_backward(grad_out: torch.Tensor, y: torch.Tensor, scatter_ind
     """Gradients of ``combine_tokens`` with respect to y and topk_weights:
     (grad_y (M * k, H), grad_weights fp32 (M, k)); the residual's is grad_out
     itself (moe_combine_tokens_backward)."""
-    _cuda_2d(grad_out, "grad_out")
-    M, k = _weights(topk_weights)
-    dev, H = grad_out.device, grad_out.shape[1]
+    dev = _rows(grad_out, "grad_out")
+    _rows(topk_weights, "topk_weights")
+    M, k = topk_weights.shape
+    H = grad_out.shape[1]
     code = _dtype_code(grad_out)
-    _expect(grad_out, "grad_out", (M, H), grad_out.dtype, topk_weights.device)
+    if grad_out.shape[0] != M:
+        raise ValueError(f"grad_out must have a row for each of the {M} tokens")
+    _expect(topk_weights, "topk_weights", (M, k), torch.float32, dev)
     _expect(y, "y", (M * k, H), grad_out.dtype, dev)
     _scatter(scatter_indx, M * k, dev)
     grad_y = _like(grad_y, "grad_y", y, (M * k, H), y.dtype)
@@ -162,21 +166,24 @@ def combine_tokens_backward(grad_out: torch.Tensor, y: torch.Tensor, scatter_ind
     return grad_y, grad_weights
 
 
-def _experts(rows: torch.Tensor, name: str, expert_offsets: torch.Tensor) -> int:
-    """Checks of a sorted row array and the offsets; the number of experts."""
-    _cuda_2d(rows, name)
-    _bf16(rows, name)
-    if expert_offsets.dtype != torch.int32 or expert_offsets.dim() != 1 or expert_offsets.numel() < 2 or \
-            not expert_offsets.is_contiguous():
-        raise ValueError("expert_offsets must be a contiguous int32 tensor of E + 1 values")
-    _same_device(rows.device, expert_offsets=expert_offsets)
-    return expert_offsets.numel() - 1
+def _experts(rows: torch.Tensor, name: str, expert_offsets: torch.Tensor):
+    """Checks of a sorted row array and the offsets; the device's number and
+    the number of experts."""
+    index = _rows(rows, name)
+    if rows.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16")
+    if not (expert_offsets.dtype is torch.int32 and expert_offsets.dim() == 1 and expert_offsets.numel() >= 2
+            and expert_offsets.is_contiguous() and expert_offsets.get_device() == index):
+        raise ValueError(f"expert_offsets must be a contiguous int32 tensor of E + 1 values on cuda:{index}")
+    return index, expert_offsets.numel() - 1
 
 
-def _weight(weight: torch.Tensor, E: int, device) -> None:
-    if weight.dim() != 3 or weight.shape[0] != E or weight.dtype != torch.bfloat16 or not weight.is_contiguous() or \
-            weight.device != device:
-        raise ValueError(f"weight must be a contiguous bfloat16 tensor (E = {E}, N, K) on {device}")
+def _weight(weight: torch.Tensor, E: int, index: int):
+    """(N, K) of a weight."""
+    if not (weight.dtype is torch.bfloat16 and weight.dim() == 3 and weight.is_contiguous()
+            and weight.get_device() == index and weight.shape[0] == E):
+        raise ValueError(f"weight must be a contiguous bfloat16 tensor (E = {E}, N, K) on cuda:{index}")
+    return weight.shape[1:]
 
 
 def expert_matmul(x: torch.Tensor, weight: torch.Tensor, expert_offsets: torch.Tensor, bias=None,
@@ -189,12 +196,11 @@ def expert_matmul(x: torch.Tensor, weight: torch.Tensor, expert_offsets: torch.T
     (P, N) or, with ``return_preact`` or ``preact_out``, (out, preact): the
     activation's input, for the backward pass.  A plain matrix product is
     E = 1 with offsets [0, P]."""
-    E = _experts(x, "x", expert_offsets)
+    dev, E = _experts(x, "x", expert_offsets)
     act, gated = _activation(activation), bool(gated)
-    dev, (P, K) = x.device, x.shape
-    _weight(weight, E, dev)
-    Nz = weight.shape[1]
-    if weight.shape[2] != K or (gated and Nz % 2):
+    P, K = x.shape
+    Nz, Kw = _weight(weight, E, dev)
+    if Kw != K or (gated and Nz % 2):
         raise ValueError("weight does not match x's columns, or a gated weight has an odd number of rows")
     N = Nz // 2 if gated else Nz
     if bias is not None:
@@ -217,13 +223,12 @@ def expert_matmul_grad_input(grad_out: torch.Tensor, weight: torch.Tensor, exper
     rows: grad_out (P, N) times weight (E, N, K), taken on through the
     activation that made those rows if ``preact``, (P, K) or gated (P, 2 K), is
     given: the result then has preact's shape (moe_expert_matmul_grad_input)."""
-    E = _experts(grad_out, "grad_out", expert_offsets)
+    dev, E = _experts(grad_out, "grad_out", expert_offsets)
     act, gated = _activation(activation), bool(gated)
-    dev, (P, N) = grad_out.device, grad_out.shape
-    _weight(weight, E, dev)
-    if weight.shape[1] != N:
+    P, N = grad_out.shape
+    Nw, K = _weight(weight, E, dev)
+    if Nw != N:
         raise ValueError("weight does not match grad_out's columns")
-    K = weight.shape[2]
     shape = (P, 2 * K if gated else K)
     if preact is not None:
         _expect(preact, "preact", shape, torch.bfloat16, dev)
@@ -241,8 +246,8 @@ def expert_matmul_grad_weight(grad_out: torch.Tensor, x: torch.Tensor, expert_of
     weight: (E, N, K) of ``dtype`` (bfloat16 or float32) from grad_out (P, N)
     and x (P, K); with ``bias_grad`` also the bias's, fp32 (E, N).  Experts
     without rows get zeros (moe_expert_matmul_grad_weight)."""
-    E = _experts(grad_out, "grad_out", expert_offsets)
-    dev, (P, N) = grad_out.device, grad_out.shape
+    dev, E = _experts(grad_out, "grad_out", expert_offsets)
+    P, N = grad_out.shape
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     K = x.shape[1]
@@ -263,9 +268,9 @@ def topk_backward(grad_weights: torch.Tensor, gating_output: torch.Tensor, topk_
     (moe_topk_backward).  ``scoring``: "softmax" (``topk_softmax``,
     ``grouped_topk``) or "sigmoid" (``biased_grouped_topk``, fused routers);
     the other arguments as in the routing call."""
-    _cuda_2d(gating_output, "gating_output")
+    dev = _rows(gating_output, "gating_output")
     M, E = gating_output.shape
-    dev, code = gating_output.device, _dtype_code(gating_output)
+    code = _dtype_code(gating_output)
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {sorted(SCORINGS)}, not {scoring!r}")
     if topk_ids.dim() != 2:

@@ -125,6 +125,9 @@ class OnGpu:
     def __init__(self, t, device="cuda:0"):
         self.t, self.device, self.is_cuda = t, torch.device(device), True
 
+    def get_device(self):
+        return self.device.index
+
     def __getattr__(self, name):
         return getattr(self.t, name)
 
