@@ -57,6 +57,7 @@ constexpr int kM = 128;                 // accumulator lanes: weight rows
 constexpr int kBK = 64;                 // reduction per stage (one 128-byte swizzle row)
 constexpr int kABytes = kM * kBK * 2;
 constexpr int kAccCols = 256;           // TMEM columns of one accumulator
+constexpr int kUnit = 32;               // token step of a pair's product
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
@@ -75,7 +76,6 @@ struct RowArgs {
     int red;             // reduction length
     int tiles_f;         // pairs of feature tiles
     int tn_max;          // tokens per tile at most
-    int box;             // token rows per TMA copy
     int stages, stage_bytes;
     int N;               // columns of one output part
     const float* bias;   // (E, N) or (E, 2 N)
@@ -118,15 +118,30 @@ __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
-// Position in a ring of `n` barriers: index and phase parity, stepped without
-// division (a division by the runtime stage count costs an issuing lane more
-// than the four products of a stage).
+// Position in a ring of two accumulators.
 struct Ring {
     int s = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void step(int n) {
         if (++s == n) {
             s = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Position in the ring of stages: byte offset of the stage, of its barrier in
+// each row of barriers, and the phase parity.  An issuing lane is one thread,
+// whose dependent instructions take 4 cycles and more each: divisions by the
+// stage count cost it more than a stage's products, and so do descriptors put
+// together anew for each product.
+struct Stages {
+    uint32_t at = 0, bar = 0, phase = 0;
+    __device__ __forceinline__ void step(uint32_t bytes, uint32_t all) {
+        at += bytes;
+        bar += 8;
+        if (at == all) {
+            at = bar = 0;
             phase ^= 1;
         }
     }
@@ -193,7 +208,7 @@ struct Tile {
     int f;      // feature tile of this CTA of the pair
     int row0;   // first token row
     int valid;  // tokens of the tile
-    int tn;     // valid rounded up to 32
+    int tn;     // valid rounded up to kUnit
 };
 
 // Tiles run over experts, then feature tiles, then the token tiles of the
@@ -212,11 +227,13 @@ __device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int
     const int f_pair = (int)(in / parts);
     t.f = 2 * f_pair + rank;
     const int part = (int)(in - (int64_t)f_pair * parts);
-    const int step = ((s.count[lo] + parts - 1) / parts + 31) & ~31;
-    t.row0 = s.begin[lo] + part * step;
-    const int left = s.count[lo] - part * step;
-    t.valid = left < step ? left : step;
-    t.tn = (t.valid + 31) & ~31;
+    // equal parts to within one unit of 32 tokens
+    const int units = (s.count[lo] + kUnit - 1) / kUnit, q = units / parts, more = units - q * parts;
+    const int first = part * q + (part < more ? part : more);
+    t.row0 = s.begin[lo] + first * kUnit;
+    t.tn = (q + (part < more ? 1 : 0)) * kUnit;
+    const int left = s.count[lo] - first * kUnit;
+    t.valid = left < t.tn ? left : t.tn;
     return t;
 }
 
@@ -507,20 +524,10 @@ __device__ __forceinline__ void end_block(uint32_t tmem, int warp) {
     }
 }
 
-// Expects the copies of stage s in both CTAs (`bytes` each) on the even one's
-// barrier, whose address it gives.  Only the even CTA arrives: its barrier
-// cannot complete before, however early the other's copies land.  (An arrival
-// of the other one, a release at cluster scope, costs its producer more than a
-// stage's products: 2.90 against 1.72 ms for the first product of 4096 x 8
-// rows.)
-__device__ __forceinline__ uint32_t expect_pair(Control* c, int s, int rank, uint32_t bytes) {
-    if (rank == 0) ptx::mbar_arrive_expect_tx(&c->full[s], 2 * bytes);
-    return ptx::map_to_rank(ptx::smem_u32(&c->full[s]), 0);
-}
-
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, RowArgs a) {
+    expert_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmX16, RowArgs a) {
     constexpr bool GRAD = MODE == kGrad || MODE == kGradGated;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = ptx::smem_align<1024>(smem_raw);
@@ -534,49 +541,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmW);
         ptx::tma_prefetch_desc(&tmX);
+        ptx::tma_prefetch_desc(&tmX16);
     }
     const uint32_t tmem = start_block(c, a.stages, warp);
     ptx::griddep_wait();
     load_segments(seg, a.off, a.E, a.P, a.tn_max);
     const int64_t tiles = (int64_t)seg.cum[a.E] * a.tiles_f;
 
-    if (warp == 0) {
+    const uint32_t ring_at = ptx::smem_u32(ring), all = a.stages * a.stage_bytes;
+    const uint32_t full = ptx::smem_u32(c->full), empty = ptx::smem_u32(c->empty);
+    if (warp == 0 || warp == 3) {
+        // Producers: warp 0 copies the weight's tile, warp 3 the tokens', both
+        // to the even CTA's barrier.  One lane for both is late: a copy takes
+        // it some 80 cycles to issue.
         if (elect_one()) {
-            Ring r;
+            Stages r;
             bool ok = true;
+            const uint32_t full_pair = ptx::map_to_rank(full, 0);
             for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                 const Tile t = tile_at(seg, a, tile, rank);
                 const int row0 = t.row0 + rank * (t.tn / 2);  // this CTA's half of the tokens
-                const int boxes = (t.tn / 2 + a.box - 1) / a.box;
-                const uint32_t bytes = kABytes + boxes * a.box * kBK * 2;
-                for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
-                    if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
+                const uint32_t bytes = 2 * kABytes + t.tn * (kBK * 2);
+                for (int k = 0; k < a.red; k += kBK, r.step(a.stage_bytes, all)) {
+                    if (!ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
-                    uint8_t* a_s = ring + r.s * a.stage_bytes;
-                    uint8_t* b_s = a_s + kABytes;
-                    const uint32_t full = expect_pair(c, r.s, rank, bytes);
-                    if constexpr (GRAD) {
-                        ptx::tma_load(a_s, &tmW, t.f * kM, k, t.e, full);
-                        ptx::tma_load(a_s + kABytes / 2, &tmW, t.f * kM + 64, k, t.e, full);
-                    } else if constexpr (MODE == kFwdGated) {
-                        ptx::tma_load(a_s, &tmW, k, 0, 0, t.f * 8, t.e, full);
+                    const uint32_t at = ring_at + r.at, bar = full_pair + r.bar;
+                    if (warp == 0) {
+                        // Only the even CTA arrives: its barrier cannot complete
+                        // before, however early the other's copies land.  (An
+                        // arrival of the other one, a release at cluster scope,
+                        // takes longer than a stage's products: 2.90 against
+                        // 1.72 ms for the first product of 4096 x 8 rows.)
+                        if (rank == 0) ptx::bar_expect(full + r.bar, bytes);
+                        if constexpr (GRAD) {
+                            ptx::tma_load(at, &tmW, t.f * kM, k, t.e, bar);
+                            ptx::tma_load(at + kABytes / 2, &tmW, t.f * kM + 64, k, t.e, bar);
+                        } else if constexpr (MODE == kFwdGated) {
+                            ptx::tma_load(at, &tmW, k, 0, 0, t.f * 8, t.e, bar);
+                        } else {
+                            ptx::tma_load(at, &tmW, k, t.f * kM, t.e, bar);
+                        }
                     } else {
-                        ptx::tma_load(a_s, &tmW, k, t.f * kM, t.e, full);
+                        uint32_t to = at + kABytes;
+                        int row = row0;
+                        for (int i = t.tn / 64; i > 0; --i, row += 32, to += 32 * kBK * 2)
+                            ptx::tma_load(to, &tmX, k, row, bar);
+                        if (t.tn & 32) ptx::tma_load(to, &tmX16, k, row, bar);
                     }
-                    for (int i = 0; i < boxes; ++i)
-                        ptx::tma_load(b_s + i * a.box * kBK * 2, &tmX, k, row0 + i * a.box, full);
                 }
             }
             // Leave only once every stage filled has been used, or its wait has run out.
-            for (int i = 0; i < a.stages; ++i, r.step(a.stages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
+            for (int i = 0; i < a.stages; ++i, r.step(a.stage_bytes, all))
+                ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
-            Ring r, acc;
+            Stages r;
+            Ring acc;
             bool ok = true;
+            // descriptors of the first stage's operands; steps of 16 in the reduction
+            const uint64_t ad0 = GRAD ? ptx::sdesc_sw128(ring_at, kABytes / 2, 1024) : ptx::sdesc_sw128(ring_at, 16, 1024);
+            const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 16, 1024);
+            constexpr uint64_t A_STEP = GRAD ? 2048 >> 4 : 32 >> 4, B_STEP = 32 >> 4;
             for (int64_t tile = pair; tile < tiles && ok; tile += pairs, acc.step(2)) {
                 const Tile t = tile_at(seg, a, tile, rank);
                 const uint32_t idesc = ptx::idesc_bf16_m256(t.tn, GRAD, false);
@@ -586,25 +615,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
-                for (int k = 0; k < a.red; k += kBK, r.step(a.stages)) {
-                    if (!ptx::mbar_wait_cluster(&c->full[r.s], r.phase, kWaitNs)) {
+                for (int k = 0; k < a.red; k += kBK, r.step(a.stage_bytes, all)) {
+                    if (!ptx::bar_wait<true>(full + r.bar, r.phase, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t a_addr = ptx::smem_u32(ring + r.s * a.stage_bytes);
-                    const uint32_t b_addr = a_addr + kABytes;
+                    const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t ad = GRAD ? ptx::sdesc_sw128(a_addr + kk * 2048, kABytes / 2, 1024)
-                                                 : ptx::sdesc_sw128(a_addr + kk * 32, 16, 1024);
-                        ptx::umma_bf16_pair(d, ad, ptx::sdesc_sw128(b_addr + kk * 32, 16, 1024), idesc,
-                                            (k | kk) != 0);
-                    }
-                    ptx::umma_commit_pair(&c->empty[r.s]);
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        ptx::umma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, (k | kk) != 0);
+                    ptx::umma_commit_pair(empty + r.bar);
                 }
-                ptx::umma_commit_pair(&c->acc_full[acc.s]);
+                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]));
             }
         }
     } else if (warp >= 4) {
@@ -691,44 +715,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_e = a.tiles_n * a.tiles_k;
     const int64_t tiles = (int64_t)a.E * per_e;
 
-    if (warp == 0) {
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    const uint32_t full = ptx::smem_u32(c->full), tail = ptx::smem_u32(c->tail), cut = ptx::smem_u32(c->cut),
+                   empty = ptx::smem_u32(c->empty);
+    constexpr uint32_t all = kWStages * kWStageBytes;
+    if (warp == 0 || warp == 2) {
+        // Producers: warp 0 copies grad_out's tile, warp 2 x's.
         if (elect_one()) {
-            Ring r;
+            Stages r;
             bool ok = true;
+            const uint32_t full_pair = ptx::map_to_rank(full, 0);
+            const CUtensorMap* tm = warp == 0 ? &tmY : &tmX;
+            const uint32_t part = ring_at + (warp == 0 ? 0 : kABytes);
             for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                 const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
-                const int n0 = (in / a.tiles_k * 2 + rank) * kM, k0 = in % a.tiles_k * kWN + rank * (kWN / 2);
-                for (int p = 0; p < seg.count[e]; p += kBK, r.step(kWStages)) {
-                    if (!ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs)) {
+                const int c0 = warp == 0 ? (in / a.tiles_k * 2 + rank) * kM : in % a.tiles_k * kWN + rank * (kWN / 2);
+                const int count = seg.count[e], row0 = seg.begin[e];
+                for (int p = 0; p < count; p += kBK, r.step(kWStageBytes, all)) {
+                    if (!ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
-                    uint8_t* a_s = ring + r.s * kWStageBytes;
-                    const int row = seg.begin[e] + p;
-                    uint32_t full;
-                    if (seg.count[e] - p >= kBK) {
-                        full = expect_pair(c, r.s, rank, kWStageBytes);
-                    } else {  // warp 3 goes over this one first
-                        full = ptx::smem_u32(&c->tail[r.s]);
-                        ptx::mbar_arrive_expect_tx(&c->tail[r.s], kWStageBytes);
+                    // a whole stage counts in the even CTA, for both; over one
+                    // that ends a segment this CTA's warp 3 goes first
+                    const bool whole = count - p >= kBK;
+                    const uint32_t bar = whole ? full_pair + r.bar : tail + r.bar;
+                    if (warp == 0) {
+                        if (!whole) ptx::bar_expect(tail + r.bar, kWStageBytes);
+                        else if (rank == 0) ptx::bar_expect(full + r.bar, 2 * kWStageBytes);
                     }
-#pragma unroll
-                    for (int i = 0; i < kM / 64; ++i)
-                        ptx::tma_load(a_s + i * 8192, &tmY, n0 + i * 64, row, full);
-#pragma unroll
-                    for (int i = 0; i < kWN / 128; ++i)
-                        ptx::tma_load(a_s + kABytes + i * 8192, &tmX, k0 + i * 64, row, full);
+                    ptx::tma_load(part + r.at, tm, c0, row0 + p, bar);
+                    ptx::tma_load(part + r.at + 8192, tm, c0 + 64, row0 + p, bar);
                 }
             }
-            for (int i = 0; i < kWStages; ++i, r.step(kWStages)) ptx::mbar_wait(&c->empty[r.s], r.phase ^ 1, kWaitNs);
+            for (int i = 0; i < kWStages; ++i, r.step(kWStageBytes, all))
+                ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs);
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_m256(kWN, true, true);
-            Ring r, acc;
-            uint32_t uses[2] = {0, 0};  // parity of each stage's uses: whole, as a tail
+            Stages r;
+            Ring acc;
+            uint32_t whole_uses = 0, tail_uses = 0;  // parity of each stage's uses (bit of its barrier's offset)
             bool ok = true;
+            const uint64_t ad0 = ptx::sdesc_sw128(ring_at, 8192, 1024);
+            const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 8192, 1024);
             for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                 const int count = seg.count[(int)(tile / per_e)];
                 if (count == 0) continue;
@@ -738,55 +770,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
-                for (int p = 0; p < count; p += kBK, r.step(kWStages)) {
+                for (int p = 0; p < count; p += kBK, r.step(kWStageBytes, all)) {
+                    const uint32_t bit = r.bar >> 3;
                     const bool whole = count - p >= kBK;
-                    uint32_t& use = uses[whole ? 0 : 1];
-                    if (!ptx::mbar_wait_cluster(whole ? &c->full[r.s] : &c->cut[r.s], use >> r.s & 1, kWaitNs)) {
+                    ok = whole ? ptx::bar_wait<true>(full + r.bar, whole_uses >> bit & 1, kWaitNs)
+                               : ptx::bar_wait<true>(cut + r.bar, tail_uses >> bit & 1, kWaitNs);
+                    if (!ok) {
                         give_up(abort_flag);
-                        ok = false;
                         break;
                     }
-                    use ^= 1u << r.s;
+                    if (whole) whole_uses ^= 1u << bit;
+                    else tail_uses ^= 1u << bit;
                     ptx::tc_fence_after();
-                    const uint32_t a_addr = ptx::smem_u32(ring + r.s * kWStageBytes), b_addr = a_addr + kABytes;
+                    const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
                     const int steps = steps_of(count - p);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         if (kk < steps)
-                            ptx::umma_bf16_pair(d, ptx::sdesc_sw128(a_addr + kk * 2048, 8192, 1024),
-                                                ptx::sdesc_sw128(b_addr + kk * 2048, 8192, 1024), idesc,
-                                                (p | kk) != 0);
-                    ptx::umma_commit_pair(&c->empty[r.s]);
+                            ptx::umma_bf16_pair(d, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), idesc, (p | kk) != 0);
+                    ptx::umma_commit_pair(empty + r.bar);
                 }
-                ptx::umma_commit_pair(&c->acc_full[acc.s]);
+                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]));
                 acc.step(2);
             }
         }
     } else if (warp == 3) {
         // The last stage of a segment holds rows of the next one: zero them in
         // every box, then arrive for this CTA.
-        Ring r;
+        Stages r;
         uint32_t uses = 0;  // parity of each stage's uses as a tail
         bool ok = true;
         for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
             const int count = seg.count[(int)(tile / per_e)], left = count % kBK;
-            for (int p = kBK; p <= count; p += kBK) r.step(kWStages);
+            for (int p = kBK; p <= count; p += kBK) r.step(kWStageBytes, all);
             if (left == 0) continue;
-            if (!ptx::mbar_wait(&c->tail[r.s], uses >> r.s & 1, kWaitNs)) {
+            const uint32_t bit = r.bar >> 3;
+            if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs)) {
                 if (lane == 0) give_up(abort_flag);
                 ok = false;
                 break;
             }
-            uses ^= 1u << r.s;
-            uint8_t* a_s = ring + r.s * kWStageBytes;
+            uses ^= 1u << bit;
+            uint8_t* a_s = ring + r.at;
             const int pieces = (16 * steps_of(left) - left) * 8;  // 16-byte pieces per 64-column box
             for (int i = lane; i < pieces * (kWStageBytes / 8192); i += 32)
                 *reinterpret_cast<uint4*>(a_s + (i / pieces) * 8192 + left * 128 + (i % pieces) * 16) =
                     make_uint4(0, 0, 0, 0);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->cut[r.s]), 0));
-            r.step(kWStages);
+            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(cut + r.bar, 0));
+            r.step(kWStageBytes, all);
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
@@ -947,7 +980,6 @@ static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + kTail <= kSmemMax, "row pro
 void choose_tile(RowArgs& a) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
-    a.box = a.tn_max <= 64 ? 16 : 32;
     a.stage_bytes = kABytes + a.tn_max / 2 * kBK * 2;
     const int fit = (int)((kSmemMax - 1024 - kTail) / a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
@@ -960,11 +992,12 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     if (rc != MOE_OK) return rc;
     rc = allow_smem((const void*)expert_rows_kernel<MODE>, dev, kSmemMax);
     if (rc != MOE_OK) return rc;
-    CUtensorMap tmX;
-    cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, a.box);
+    CUtensorMap tmX, tmX16;  // boxes of 32 and of 16 tokens: a CTA's half of any number of units
+    cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, 32);
+    if (err == cudaSuccess) err = encode_rows(&tmX16, x, a.P, x_cols, 16);
     if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
     const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kTail;
-    return launch(expert_rows_kernel<MODE>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmW, tmX, a);
+    return launch(expert_rows_kernel<MODE>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmW, tmX, tmX16, a);
 }
 
 bool bad(const void* p, size_t n) { return !p || reinterpret_cast<uintptr_t>(p) % n != 0; }

@@ -62,8 +62,8 @@ __device__ __forceinline__ uint32_t places(const int32_t* scatter, int64_t t, in
     return __ballot_sync(0xffffffffu, *place < P);
 }
 
-// Accesses a lane has in flight per row: 64 bytes, at most 8 accesses.
-template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : 8; }
+// Accesses a lane has in flight per row: 64 bytes, at most 16 accesses.
+template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : VB >= 8 ? 8 : 16; }
 
 // One warp per (token, segment of 32 * U accesses of the row).
 template <typename T, int VB>
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kTokThreads)
     combine_kernel(const T* y, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
                    const float* __restrict__ weights, const T* residual, T* out, int segs) {
     using C = Chunk<T, VB>;
-    constexpr int U = unroll<VB>() / 2, R = 4;
+    constexpr int U = unroll<VB>() / 2, R = VB >= 16 ? 4 : 2;
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
     ptx::griddep_wait();
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256)
                             const int32_t* __restrict__ scatter, int k, const float* __restrict__ weights, T* grad_y,
                             float* grad_weights) {
     using C = Chunk<T, VB>;
-    constexpr int U = unroll<VB>();
+    constexpr int U = VB >= 16 ? 4 : 8;
     __shared__ float s_dot[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * (8 / W) + warp / W;

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int 
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
+        if (i * 32 * N >= a.E) break;
         const int e0 = (lane + 32 * i) * N;
         union {
             uint4 v;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int 
     }
     const float total = group_sum<32>(s);
     const float p = mine ? expf(cap(raw, a.softcap) - top) / total : 0.0f;
-    const float rest = group_sum<32>(g * p);
+    const float rest = group_sum<32>(g * p), rest_total = rest / total;
     bool first;
     const float sum = joint<32>(g * p, id, mine, a.k, &first);
 #pragma unroll
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int 
         } c;
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            float t = -rest * (z[i][u] / total);
+            float t = -rest_total * z[i][u];
             if (a.softcap != 0.0f && e0 + u < a.E) t *= cap_slope(load_f32(x + e0 + u), a.softcap);
             put(&c.t[u], t);
         }
