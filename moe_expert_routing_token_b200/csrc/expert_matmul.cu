@@ -94,21 +94,39 @@ struct WeightArgs {
     float* grad_bias;
 };
 
-// The intrinsics' few units in the 24th bit vanish in the rounding to bf16.
-__device__ __forceinline__ float act_f(float z, int act) {
-    if (act == MOE_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-    if (act == MOE_ACT_GELU) return z * normcdff(z);
-    return z;
+// The normal distribution's tail over its density at t >= 0 (Mills' ratio),
+// sqrt(pi / 2) erfcx(t / sqrt 2): a rational function fitted here by weighted
+// least squares to a relative error of 7e-7 (in fp32) up to t = 14, where the
+// density leaves fp32.  With it Phi(-t) keeps its relative precision far out,
+// in 8 multiply-adds and a division; normcdff's several branches made the
+// epilogue of 32 x 32 values last longer than its tile's products.
+__device__ __forceinline__ float mills(float t) {
+    const float p = fmaf(fmaf(fmaf(0.04273192584514618f, t, 0.2996203303337097f), t, 0.9073256254196167f), t,
+                         1.253313660621643f);
+    const float q = fmaf(fmaf(fmaf(fmaf(0.042736925184726715f, t, 0.2994176745414734f), t, 0.9534378051757812f), t,
+                              1.5218068361282349f), t, 1.0f);
+    return __fdividef(p, q);
 }
 
-__device__ __forceinline__ float act_df(float z, int act) {
+// f(z), and f'(z) where asked for.  The intrinsics' few units in the 24th bit
+// vanish in the rounding to bf16.  (|z| is cut at 14 by a comparison, which
+// leaves a NaN one.)
+template <bool GRAD>
+__device__ __forceinline__ float2 act_both(float z, int act) {
     if (act == MOE_ACT_SILU) {
         const float p = __fdividef(1.0f, 1.0f + __expf(-z));
-        return p * (1.0f + z * (1.0f - p));
+        return make_float2(z * p, GRAD ? p * fmaf(z, 1.0f - p, 1.0f) : 0.0f);
     }
-    if (act == MOE_ACT_GELU) return normcdff(z) + z * 0.3989422804014327f * expf(-0.5f * z * z);
-    return 1.0f;
+    if (act == MOE_ACT_GELU) {
+        const float u = fabsf(z), t = u > 14.0f ? 14.0f : u;
+        const float density = 0.3989422804014327f * __expf(-0.5f * t * t);
+        const float tail = density * mills(t);  // Phi(-|z|)
+        return make_float2(fmaf(0.5f, u, 0.5f * z) - t * tail,
+                           GRAD ? fmaf(copysignf(t, z), density, z < 0.0f ? tail : 1.0f - tail) : 0.0f);
+    }
+    return make_float2(z, 1.0f);
 }
+__device__ __forceinline__ float act_f(float z, int act) { return act_both<false>(z, act).x; }
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -302,13 +320,52 @@ __device__ __forceinline__ void get16(uint32_t stage, uint32_t (&w)[4][2], int l
         ptx::ldmatrix_x4_trans(at + 8 * i * kPitch, w[i][0], w[i][1], w[i + 1][0], w[i + 1][1]);
 }
 
+// First output column of a quarter's 32 lanes.
+template <int MODE>
+__device__ __forceinline__ int first_column(const Tile& t, int quarter) {
+    return MODE == kFwdGated ? t.f * 64 + quarter * 16 : t.f * kM + quarter * 32;
+}
+
+// The bias of this thread's fragment rows: features l / 4 + 8 m, when gated of
+// the gate (m 0, 1) and of the other factor (m 2, 3).
+template <int MODE>
+struct Bias {
+    float b[4];
+    __device__ __forceinline__ void load(const RowArgs& a, const Tile& t, int quarter, int lane) {
+        if (MODE != kFwd && MODE != kFwdGated) return;
+        if (a.bias == nullptr) return;
+        const int col0 = first_column<MODE>(t, quarter) + lane / 4;
+        const float* row = a.bias + (int64_t)t.e * (MODE == kFwdGated ? 2 : 1) * a.N;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int c = col0 + 8 * (MODE == kFwdGated ? m % 2 : m);
+            b[m] = c < a.N ? __ldg(row + (MODE == kFwdGated ? m / 2 * a.N : 0) + c) : 0.0f;
+        }
+    }
+};
+
+// Bring the rows that the tile's epilogue reads (64 bytes a token and part)
+// into L2 while its products are still running.
+template <int MODE>
+__device__ __forceinline__ void prefetch_extra(const RowArgs& a, const Tile& t, int quarter, int half, int lane) {
+    if (a.extra == nullptr) return;
+    const int col0 = first_column<MODE>(t, quarter);
+    if (col0 >= a.N) return;
+    const int64_t ld = MODE == kGradGated ? 2 * (int64_t)a.N : a.N;
+    for (int tok = half * 32 + lane; tok < t.valid; tok += 64) {
+        const bf16* p = a.extra + ((int64_t)t.row0 + tok) * ld + col0;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+        if constexpr (MODE == kGradGated) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + a.N));
+    }
+}
+
 // One warp's 32 lanes x 32 tokens of the accumulator at taddr.
 template <int MODE>
-__device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, uint32_t taddr, int tok0, int quarter,
-                                               uint8_t* stage, int lane) {
+__device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, const Bias<MODE>& bias, uint32_t taddr,
+                                               int tok0, int quarter, uint8_t* stage, int lane) {
     constexpr int WIDTH = MODE == kFwdGated ? 32 : 64;       // bytes of one output part per token
     const int valid = t.valid - tok0;                        // tokens of this chunk (may exceed 32)
-    const int col0 = MODE == kFwdGated ? t.f * 64 + quarter * 16 : t.f * kM + quarter * 32;
+    const int col0 = first_column<MODE>(t, quarter);
     const int cols = a.N - col0;                             // columns left (may be <= 0)
     const int64_t row0 = (int64_t)t.row0 + tok0;
     const uint32_t sst = ptx::smem_u32(stage);
@@ -327,15 +384,12 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
         uint32_t w[4][4] = {};
         if (a.bias != nullptr) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int c = 8 * m + lane / 4;
-                const float b = c < cols ? __ldg(a.bias + (int64_t)t.e * a.N + col0 + c) : 0.0f;
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[m / 2][i][2 * (m % 2)] += b;
-                    acc[m / 2][i][2 * (m % 2) + 1] += b;
+                    acc[m / 2][i][2 * (m % 2)] += bias.b[m];
+                    acc[m / 2][i][2 * (m % 2) + 1] += bias.b[m];
                 }
-            }
         }
         if (a.preact != nullptr) {
 #pragma unroll
@@ -375,18 +429,14 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
         const int64_t ld_z = 2 * (int64_t)a.N;
         if (a.bias != nullptr) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = 8 * h + lane / 4;
-                const float* b = a.bias + (int64_t)t.e * ld_z + col0 + c;
-                const float bg = c < cols ? __ldg(b) : 0.0f, bu = c < cols ? __ldg(b + a.N) : 0.0f;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[h][i][0] += bg;
-                    acc[h][i][1] += bg;
-                    acc[h][i][2] += bu;
-                    acc[h][i][3] += bu;
+                    acc[h][i][0] += bias.b[h];
+                    acc[h][i][1] += bias.b[h];
+                    acc[h][i][2] += bias.b[2 + h];
+                    acc[h][i][3] += bias.b[2 + h];
                 }
-            }
         }
         uint32_t w[4][2] = {};
         if (a.preact != nullptr) {
@@ -448,14 +498,15 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 float x = acc[m / 2][i][2 * (m % 2)], y = acc[m / 2][i][2 * (m % 2) + 1];
                 if (a.extra != nullptr) {
                     const float2 z = unpack(g[i][m]);
+                    const float2 fx = act_both<true>(z.x, a.act), fy = act_both<true>(z.y, a.act);
                     if constexpr (MODE == kGradGated) {
                         const float2 v = unpack(u[i][m]);
-                        u[i][m] = pack(x * act_f(z.x, a.act), y * act_f(z.y, a.act));
+                        u[i][m] = pack(x * fx.x, y * fy.x);
                         x *= v.x;
                         y *= v.y;
                     }
-                    x *= act_df(z.x, a.act);
-                    y *= act_df(z.y, a.act);
+                    x *= fx.y;
+                    y *= fy.y;
                 }
                 w[i][m] = pack(x, y);
             }
@@ -637,6 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring acc;
         for (int64_t tile = pair; tile < tiles; tile += pairs, acc.step(2)) {
             const Tile t = tile_at(seg, a, tile, rank);
+            Bias<MODE> bias;
+            bias.load(a, t, quarter, lane);
+            prefetch_extra<MODE>(a, t, quarter, half, lane);
             if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
                 if (lane == 0) give_up(abort_flag);
                 *abort_flag = 1;
@@ -646,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t base = tmem + acc.s * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
             for (int tok0 = half * 32; tok0 < t.valid; tok0 += 64)
-                epilogue_chunk<MODE>(a, t, base + tok0, tok0, quarter, stage, lane);
+                epilogue_chunk<MODE>(a, t, bias, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
