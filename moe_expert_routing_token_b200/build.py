@@ -1,8 +1,9 @@
-"""Build libmoe_routing.so (sm_100a) in-tree with nvcc.
+"""Build libmoe_routing.so (sm_100a) in-tree with nvcc, and the native part of
+the Python binding (_experts.so).
 
 Usage: ``python -m moe_expert_routing_token_b200.build`` (or call
-:func:`build`).  The library lands in ``moe_expert_routing_token_b200/_lib/``
-next to the binding that loads it.
+:func:`build`).  Both land in ``moe_expert_routing_token_b200/_lib/`` next to
+the binding that loads them.
 """
 from __future__ import annotations
 
@@ -10,6 +11,9 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_routing.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_experts.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -31,17 +37,45 @@ def sources() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(LIB_PATH, deps)
+
+
+def _older(path: str, deps: list[str]) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
+def _binding_stale() -> bool:
+    return _older(BINDING_PATH, [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _binding_command(out: str) -> list[str]:
+    # nvcc as the driver: the host compiler, and with it the C++ runtime that
+    # torch's exceptions cross, is then the library's own
+    home = os.path.dirname(torch.__file__)
+    return [os.environ.get("NVCC", "nvcc"), "-O2", "-std=c++17", "-shared", "-cudart", "none",
+            "-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            "-I", os.path.join(home, "include"),
+            "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], BINDING, "-o", out,
+            "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            LIB_PATH, "-Xlinker", "-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every CUDA source for sm_100a and link the shared library."""
-    if not force and not _stale():
-        return LIB_PATH
+    """Compile every CUDA source for sm_100a, link the shared library, and
+    compile the binding against it."""
+    if force or _stale():
+        _build_library(verbose, jobs)
+    if force or _binding_stale():
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        subprocess.run(_binding_command(tmp), check=True)
+        os.replace(tmp, BINDING_PATH)
+    return LIB_PATH
+
+
+def _build_library(verbose: bool, jobs: int) -> None:
     nvcc = os.environ.get("NVCC", "nvcc")
     obj_dir = os.path.join(PKG, "_build")
     os.makedirs(obj_dir, exist_ok=True)
@@ -61,9 +95,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     _drain(procs, verbose)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs,
-                    "-o", tmp], check=True)
+                    "-Xlinker", "-soname=libmoe_routing.so", "-o", tmp], check=True)
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 def _drain(procs, verbose):

@@ -1,7 +1,5 @@
 """Refusals of the expert layer's calls: by the C library before any CUDA
 call, and by the binding (CPU only)."""
-import ctypes
-
 import pytest
 import torch
 
@@ -118,59 +116,78 @@ def test_topk_backward(lib):
     assert call(M=0, g=None, x=None, ids=None, out=None) == 0
 
 
-class OnGpu:
-    """A CPU tensor that says it is a CUDA tensor: the binding's own checks
-    come before the library sees a pointer."""
-
-    def __init__(self, t, device="cuda:0"):
-        self.t, self.device, self.is_cuda = t, torch.device(device), True
-
-    def get_device(self):
-        return self.device.index
-
-    def __getattr__(self, name):
-        return getattr(self.t, name)
+def t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
 
 
-def gpu(*shape, dtype=torch.bfloat16, device="cuda:0"):
-    return OnGpu(torch.zeros(*shape, dtype=dtype), device)
+I32, I64, F16, F32 = torch.int32, torch.int64, torch.float16, torch.float32
 
 
-I32, F32 = torch.int32, torch.float32
-
-
-@pytest.mark.parametrize("call", [
-    lambda: moe.gather_tokens(torch.zeros(4, 8), torch.zeros(8, dtype=I32), 2),                   # not on a GPU
-    lambda: moe.gather_tokens(OnGpu(torch.zeros(8, 4).T), gpu(8, dtype=I32), 2),                  # not contiguous
-    lambda: moe.gather_tokens(gpu(4, 8, dtype=torch.float16), gpu(8, dtype=I32), 2),              # type
-    lambda: moe.gather_tokens(gpu(4, 8), gpu(7, dtype=I32), 2),                                   # places
-    lambda: moe.gather_tokens(gpu(4, 8), gpu(0, dtype=I32), 0),                                   # topk
-    lambda: moe.gather_tokens(gpu(4, 8), gpu(8, dtype=torch.int64), 2),
-    lambda: moe.gather_tokens(gpu(4, 8), gpu(8, dtype=I32, device="cuda:1"), 2),                  # another device
-    lambda: moe.gather_tokens(gpu(4, 8), gpu(8, dtype=I32), 2, out=gpu(4, 8)),                    # out's shape
-    lambda: moe.gather_tokens_backward(gpu(7, 8), gpu(7, dtype=I32), 2),
-    lambda: moe.combine_tokens(gpu(8, 8), gpu(8, dtype=I32), gpu(4, 2)),                          # weights' type
-    lambda: moe.combine_tokens(gpu(9, 8), gpu(8, dtype=I32), gpu(4, 2, dtype=F32)),
-    lambda: moe.combine_tokens(gpu(8, 8), gpu(8, dtype=I32), gpu(4, 2, dtype=F32), residual=gpu(4, 8, dtype=F32)),
-    lambda: moe.combine_tokens_backward(gpu(4, 8), gpu(8, 8, dtype=F32), gpu(8, dtype=I32), gpu(4, 2, dtype=F32)),
-    lambda: moe.expert_matmul(gpu(4, 8, dtype=F32), gpu(2, 8, 8), gpu(3, dtype=I32)),
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 16), gpu(3, dtype=I32)),                       # K
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 8), gpu(4, dtype=I32)),                        # E
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 8), gpu(1, dtype=I32)),
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 8), gpu(3, dtype=I32), activation="tanh"),
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 9, 8), gpu(3, dtype=I32), gated=True),            # odd gate
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 8), gpu(3, dtype=I32), bias=gpu(2, 8)),        # bias type
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 16, 8), gpu(3, dtype=I32), residual=gpu(4, 8)),
-    lambda: moe.expert_matmul(gpu(4, 8), gpu(2, 8, 8, device="cuda:1"), gpu(3, dtype=I32)),
-    lambda: moe.expert_matmul_grad_input(gpu(4, 8), gpu(2, 8, 8), gpu(3, dtype=I32), activation="silu"),
-    lambda: moe.expert_matmul_grad_input(gpu(4, 8), gpu(2, 8, 8), gpu(3, dtype=I32), preact=gpu(4, 8), gated=True),
-    lambda: moe.expert_matmul_grad_input(gpu(4, 8), gpu(2, 16, 8), gpu(3, dtype=I32)),
-    lambda: moe.expert_matmul_grad_weight(gpu(4, 8), gpu(5, 8), gpu(3, dtype=I32)),
-    lambda: moe.expert_matmul_grad_weight(gpu(4, 8), gpu(4, 8), gpu(3, dtype=I32), out=gpu(2, 8, 8, dtype=torch.float16)),
-    lambda: moe.topk_backward(gpu(4, 2, dtype=F32), gpu(4, 8), gpu(4, 2, dtype=I32), "tanh", True),
-    lambda: moe.topk_backward(gpu(4, 3, dtype=F32), gpu(4, 8), gpu(4, 2, dtype=I32), "softmax", True),
-    lambda: moe.topk_backward(gpu(4, 2, dtype=F32), gpu(4, 8), gpu(4, 2, dtype=torch.int64), "softmax", True),
+# The binding looks at shapes, types and layouts before the device, so CPU
+# tensors reach every refusal; right ones are refused for the device alone.
+@pytest.mark.parametrize("call,needle", [
+    (lambda: moe.gather_tokens(t(8, 4).T, t(8, dtype=I32), 2), "contiguous 2-D"),
+    (lambda: moe.gather_tokens(t(4), t(8, dtype=I32), 2), "contiguous 2-D"),
+    (lambda: moe.gather_tokens(t(4, 8, dtype=F16), t(8, dtype=I32), 2), "dtype"),
+    (lambda: moe.gather_tokens(t(4, 8), t(7, dtype=I32), 2), "scatter_indx"),
+    (lambda: moe.gather_tokens(t(4, 8), t(0, dtype=I32), 0), "positive"),
+    (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I64), 2), "scatter_indx"),
+    (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32, ), 1 << 40), "out of range"),
+    (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32), 2), "x must be a CUDA tensor"),
+    (lambda: moe.gather_tokens_backward(t(7, 8), t(7, dtype=I32), 2), "grad_sorted"),
+    (lambda: moe.gather_tokens_backward(t(8, 8), t(8, dtype=I32), 2), "CUDA"),
+    (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2)), "topk_weights"),
+    (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(8, dtype=F32)), "topk_weights"),
+    (lambda: moe.combine_tokens(t(9, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "y must have"),
+    (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32), residual=t(4, 8, dtype=F32)), "residual"),
+    (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32), residual=t(8, 8)), "residual"),
+    (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "CUDA"),
+    (lambda: moe.combine_tokens_backward(t(4, 8), t(8, 8, dtype=F32), t(8, dtype=I32), t(4, 2, dtype=F32)), "y must be"),
+    (lambda: moe.combine_tokens_backward(t(5, 8), t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "grad_out must have"),
+    (lambda: moe.combine_tokens_backward(t(4, 8), t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "CUDA"),
+    (lambda: moe.expert_matmul(t(4, 8, dtype=F32), t(2, 8, 8), t(3, dtype=I32)), "x must be bfloat16"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 16), t(3, dtype=I32)), "columns"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8, dtype=F16), t(3, dtype=I32)), "weight must be"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8).transpose(1, 2), t(3, dtype=I32)), "weight must be"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(4, dtype=I32)), "weight must be"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(1, dtype=I32)), "expert_offsets"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(3, dtype=I64)), "expert_offsets"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(3, dtype=I32), activation="tanh"), "activation"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 9, 8), t(3, dtype=I32), gated=True), "odd"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(3, dtype=I32), bias=t(2, 8)), "bias"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 16, 8), t(3, dtype=I32), residual=t(4, 8)), "residual"),
+    (lambda: moe.expert_matmul(t(4, 8), t(2, 8, 8), t(3, dtype=I32)), "CUDA"),
+    (lambda: moe.expert_matmul_grad_input(t(4, 8), t(2, 8, 8), t(3, dtype=I32), activation="silu"), "preact"),
+    (lambda: moe.expert_matmul_grad_input(t(4, 8), t(2, 8, 8), t(3, dtype=I32), gated=True), "preact"),
+    (lambda: moe.expert_matmul_grad_input(t(4, 8), t(2, 8, 8), t(3, dtype=I32), preact=t(4, 8), gated=True), "preact"),
+    (lambda: moe.expert_matmul_grad_input(t(4, 8), t(2, 16, 8), t(3, dtype=I32)), "columns"),
+    (lambda: moe.expert_matmul_grad_input(t(4, 8), t(2, 8, 8), t(3, dtype=I32)), "CUDA"),
+    (lambda: moe.expert_matmul_grad_weight(t(4, 8), t(5, 8), t(3, dtype=I32)), "x must be"),
+    (lambda: moe.expert_matmul_grad_weight(t(4, 8), t(4), t(3, dtype=I32)), "2-D"),
+    (lambda: moe.expert_matmul_grad_weight(t(4, 8), t(4, 8), t(3, dtype=I32), dtype=F16), "dtype"),
+    (lambda: moe.expert_matmul_grad_weight(t(4, 8), t(4, 8), t(3, dtype=I32), out=t(2, 8, 8, dtype=F16)), "dtype"),
+    (lambda: moe.expert_matmul_grad_weight(t(4, 8), t(4, 8), t(3, dtype=I32)), "CUDA"),
+    (lambda: moe.topk_backward(t(4, 2, dtype=F32), t(4, 8), t(4, 2, dtype=I32), "tanh", True), "scoring"),
+    (lambda: moe.topk_backward(t(4, 3, dtype=F32), t(4, 8), t(4, 2, dtype=I32), "softmax", True), "grad_weights"),
+    (lambda: moe.topk_backward(t(4, 2, dtype=F32), t(4, 8), t(4, 2, dtype=I64), "softmax", True), "topk_ids"),
+    (lambda: moe.topk_backward(t(4, 2, dtype=F32), t(4, 8), t(8, dtype=I32), "softmax", True), "topk_ids"),
+    (lambda: moe.topk_backward(t(4, 2, dtype=F32), t(4, 8), t(4, 2, dtype=I32), "softmax", True), "CUDA"),
 ])
-def test_binding(call):
-    with pytest.raises(ValueError):
+def test_binding(call, needle):
+    with pytest.raises(ValueError, match=needle):
         call()
+
+
+def test_binding_wants_tensors_and_numbers():
+    for call in (lambda: moe.gather_tokens([1], t(8, dtype=I32), 2), lambda: moe.gather_tokens(t(4, 8), None, 2),
+                 lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32), "2"),
+                 lambda: moe.topk_backward(t(4, 2, dtype=F32), t(4, 8), t(4, 2, dtype=I32), "softmax", True, "1")):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_the_binding_calls_this_library():
+    """Both bindings reach one copy of the library."""
+    with open("/proc/self/maps") as f:
+        paths = {line.split()[-1] for line in f if "libmoe_routing" in line}
+    assert len(paths) == 1

@@ -384,6 +384,20 @@ def test_topk_backward_of_the_routing_calls(dtype):
     assert float((w.to(D) - v).abs().max()) < 1e-2
 
 
+def test_operands_and_outputs_on_other_devices_are_refused():
+    x, s, w = torch.zeros(4, 8, device=DEV), torch.zeros(8, dtype=I32, device=DEV), torch.zeros(4, 2, device=DEV)
+    for call in (lambda: moe.gather_tokens(x, s.cpu(), 2), lambda: moe.gather_tokens(x, s, 2, out=torch.zeros(8, 8)),
+                 lambda: moe.gather_tokens(x, s, 2, out=torch.zeros(8, 8, dtype=BF, device=DEV)),
+                 lambda: moe.gather_tokens(x, s, 2, out=torch.zeros(8, 16, device=DEV)[:, ::2]),
+                 lambda: moe.combine_tokens(torch.zeros(8, 8, device=DEV), s, w.cpu()),
+                 lambda: moe.combine_tokens(torch.zeros(8, 8, device=DEV), s, w, residual=torch.zeros(4, 8))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(NotImplementedError, match="multiples of 8"):
+        moe.expert_matmul(torch.zeros(4, 12, dtype=BF, device=DEV), torch.zeros(1, 8, 12, dtype=BF, device=DEV),
+                          torch.zeros(2, dtype=I32, device=DEV))
+
+
 # ---------------------------------------------------------------- the calls together
 
 def layer(x, logits, W1, b1, W2, dout, k):
