@@ -90,43 +90,54 @@ struct WeightArgs {
     int64_t P;
     int E, N, K;
     int tiles_n, tiles_k;  // of 256 x 256
-    void* out;
-    float* grad_bias;
 };
 
 // The normal distribution's tail over its density at t >= 0 (Mills' ratio),
 // sqrt(pi / 2) erfcx(t / sqrt 2): a rational function fitted here by weighted
 // least squares to a relative error of 7e-7 (in fp32) up to t = 14, where the
 // density leaves fp32.  With it Phi(-t) keeps its relative precision far out,
-// in 8 multiply-adds and a division; normcdff's several branches made the
+// in 7 multiply-adds and a reciprocal; normcdff's several branches made the
 // epilogue of 32 x 32 values last longer than its tile's products.
-__device__ __forceinline__ float mills(float t) {
-    const float p = fmaf(fmaf(fmaf(0.04273192584514618f, t, 0.2996203303337097f), t, 0.9073256254196167f), t,
-                         1.253313660621643f);
-    const float q = fmaf(fmaf(fmaf(fmaf(0.042736925184726715f, t, 0.2994176745414734f), t, 0.9534378051757812f), t,
-                              1.5218068361282349f), t, 1.0f);
-    return __fdividef(p, q);
+__device__ __forceinline__ float2 mills(float2 t) {
+    using namespace ptx;
+    float2 p = fma2(t, both(0.04273192584514618f), 0.2996203303337097f);
+    p = fma2(p, t, 0.9073256254196167f);
+    p = fma2(p, t, 1.253313660621643f);
+    float2 q = fma2(t, both(0.042736925184726715f), 0.2994176745414734f);
+    q = fma2(q, t, 0.9534378051757812f);
+    q = fma2(q, t, 1.5218068361282349f);
+    q = fma2(q, t, 1.0f);
+    return mul2(p, rcp_2(q));
 }
 
-// f(z), and f'(z) where asked for.  The intrinsics' few units in the 24th bit
-// vanish in the rounding to bf16.  (|z| is cut at 14 by a comparison, which
-// leaves a NaN one.)
+// f(z) and, where asked for, f'(z) of two values.  The epilogue is bound by
+// issued instructions, hence two values an instruction wherever there is one
+// for it; the approximate exponential's and reciprocal's few units in the 24th
+// bit vanish in the rounding to bf16.  A NaN stays one.
 template <bool GRAD>
-__device__ __forceinline__ float2 act_both(float z, int act) {
+__device__ __forceinline__ float2 activate(float2 z, int act, float2* slope) {
+    using namespace ptx;
+    constexpr float kLog2e = 1.4426950408889634f;
     if (act == MOE_ACT_SILU) {
-        const float p = __fdividef(1.0f, 1.0f + __expf(-z));
-        return make_float2(z * p, GRAD ? p * fmaf(z, 1.0f - p, 1.0f) : 0.0f);
+        const float2 p = rcp_2(add2(exp2_2(mul2(z, -kLog2e)), both(1.0f)));
+        const float2 f = mul2(z, p);
+        if (GRAD) *slope = fma2(f, fma2(p, both(-1.0f), 1.0f), p);  // p + z p (1 - p)
+        return f;
     }
     if (act == MOE_ACT_GELU) {
-        const float u = fabsf(z), t = u > 14.0f ? 14.0f : u;
-        const float density = 0.3989422804014327f * __expf(-0.5f * t * t);
-        const float tail = density * mills(t);  // Phi(-|z|)
-        return make_float2(fmaf(0.5f, u, 0.5f * z) - t * tail,
-                           GRAD ? fmaf(copysignf(t, z), density, z < 0.0f ? tail : 1.0f - tail) : 0.0f);
+        const float2 u = make_float2(fabsf(z.x), fabsf(z.y));
+        const float2 t = make_float2(min_nan(u.x, 14.0f), min_nan(u.y, 14.0f));
+        const float2 density = mul2(exp2_2(mul2(mul2(t, t), -0.5f * kLog2e)), 0.3989422804014327f);
+        const float2 tail = mul2(density, mills(t));  // Phi(-|z|)
+        if (GRAD)
+            *slope = fma2(make_float2(copysignf(t.x, z.x), copysignf(t.y, z.y)), density,
+                          make_float2(z.x < 0.0f ? tail.x : 1.0f - tail.x, z.y < 0.0f ? tail.y : 1.0f - tail.y));
+        // max(z, 0) - |z| Phi(-|z|)
+        return fma2(mul2(t, -1.0f), tail, fma2(u, both(0.5f), mul2(z, 0.5f)));
     }
-    return make_float2(z, 1.0f);
+    if (GRAD) *slope = both(1.0f);
+    return z;
 }
-__device__ __forceinline__ float act_f(float z, int act) { return act_both<false>(z, act).x; }
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -413,13 +424,10 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             if (i >= groups) break;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                float x = act_f(acc[m / 2][i][2 * (m % 2)], a.act), y = act_f(acc[m / 2][i][2 * (m % 2) + 1], a.act);
-                if (a.extra != nullptr) {
-                    const float2 q = unpack(r[i][m]);
-                    x += q.x;
-                    y += q.y;
-                }
-                w[i][m] = pack(x, y);
+                const float* z = &acc[m / 2][i][2 * (m % 2)];
+                float2 v = activate<false>(make_float2(z[0], z[1]), a.act, nullptr);
+                if (a.extra != nullptr) v = ptx::add2(v, unpack(r[i][m]));
+                w[i][m] = pack(v.x, v.y);
             }
         }
         put32(sst, w, lane);
@@ -464,13 +472,10 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             if (i >= groups) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float x = act_f(acc[h][i][0], a.act) * acc[h][i][2], y = act_f(acc[h][i][1], a.act) * acc[h][i][3];
-                if (a.extra != nullptr) {
-                    const float2 q = unpack(r[i][h]);
-                    x += q.x;
-                    y += q.y;
-                }
-                w[i][h] = pack(x, y);
+                float2 v = activate<false>(make_float2(acc[h][i][0], acc[h][i][1]), a.act, nullptr);
+                v = ptx::mul2(v, make_float2(acc[h][i][2], acc[h][i][3]));
+                if (a.extra != nullptr) v = ptx::add2(v, unpack(r[i][h]));
+                w[i][h] = pack(v.x, v.y);
             }
         }
         put16(sst, w, lane);
@@ -495,20 +500,18 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             if (i >= groups) break;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                float x = acc[m / 2][i][2 * (m % 2)], y = acc[m / 2][i][2 * (m % 2) + 1];
+                float2 q = make_float2(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]);
                 if (a.extra != nullptr) {
-                    const float2 z = unpack(g[i][m]);
-                    const float2 fx = act_both<true>(z.x, a.act), fy = act_both<true>(z.y, a.act);
+                    float2 slope;
+                    const float2 f = activate<true>(unpack(g[i][m]), a.act, &slope);
                     if constexpr (MODE == kGradGated) {
-                        const float2 v = unpack(u[i][m]);
-                        u[i][m] = pack(x * fx.x, y * fy.x);
-                        x *= v.x;
-                        y *= v.y;
+                        const float2 v = unpack(u[i][m]), other = ptx::mul2(q, f);
+                        u[i][m] = pack(other.x, other.y);
+                        q = ptx::mul2(q, v);
                     }
-                    x *= fx.y;
-                    y *= fy.y;
+                    q = ptx::mul2(q, slope);
                 }
-                w[i][m] = pack(x, y);
+                w[i][m] = pack(q.x, q.y);
             }
         }
         put32(sst, w, lane);
@@ -712,48 +715,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- weight gradient
 constexpr int kWN = 256;                          // columns of a tile (K side), half in each CTA
-constexpr int kWStages = 6;
+constexpr int kWStages = 5;
+constexpr int kWEpiBytes = 32 * 128;               // staged by an epilogue warp for a tile store
 constexpr int kWStageBytes = kABytes + kWN / 2 * kBK * 2;
 
 // Products of 16 tokens for the last `left` (or 64) of a segment.
 __device__ __forceinline__ int steps_of(int left) { return left >= kBK ? kBK / 16 : (left + 15) / 16; }
 
-// 32 values of a row whose first `cols` (a multiple of 8) exist, in accesses of
-// 32 bytes: a lane has a row to itself, so each access fills a whole sector.
+// A warp's 32 rows x 128 bytes, staged in the 128-byte swizzle of its tile
+// store: lane r holds row r, whose 16-byte piece c lies at c ^ (r % 8).
 template <typename T>
-__device__ __forceinline__ void store32(T* dst, const float (&v)[32], int cols) {
-    constexpr int N = 32 / (int)sizeof(T);
-    uint32_t w[sizeof(T) * 8];
+__device__ __forceinline__ void stage_row(uint8_t* stage, const float* v, int lane) {
+    uint8_t* row = stage + lane * 128;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) * 8; ++i) {
-        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
-        else w[i] = pack(v[2 * i], v[2 * i + 1]);
-    }
-    const bool wide = reinterpret_cast<uintptr_t>(dst) % 32 == 0;
-#pragma unroll
-    for (int i = 0; i < 32 / N; ++i) {
-        const uint32_t* q = w + 8 * i;
-        if (wide && (i + 1) * N <= cols) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + i * N), "r"(q[0]),
-                         "r"(q[1]), "r"(q[2]), "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
-                         : "memory");
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (i * N + h * (N / 2) < cols)
-                    *reinterpret_cast<uint4*>(dst + i * N + h * (N / 2)) =
-                        make_uint4(q[4 * h], q[4 * h + 1], q[4 * h + 2], q[4 * h + 3]);
-        }
+    for (int c = 0; c < 8; ++c) {
+        uint4 w;
+        if constexpr (sizeof(T) == 4)
+            w = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                           __float_as_uint(v[4 * c + 3]));
+        else
+            w = make_uint4(pack(v[8 * c], v[8 * c + 1]), pack(v[8 * c + 2], v[8 * c + 3]),
+                           pack(v[8 * c + 4], v[8 * c + 5]), pack(v[8 * c + 6], v[8 * c + 7]));
+        *reinterpret_cast<uint4*>(row + ((c ^ (lane & 7)) * 16)) = w;
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_weight_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
-                         WeightArgs a) {
+                         const __grid_constant__ CUtensorMap tmOut, WeightArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = ptx::smem_align<1024>(smem_raw);
-    Control* c = reinterpret_cast<Control*>(ring + kWStages * kWStageBytes);
+    uint8_t* epi = ring + kWStages * kWStageBytes;
+    Control* c = reinterpret_cast<Control*>(epi + kEpiWarps * kWEpiBytes);
     Segments& seg = *reinterpret_cast<Segments*>(c + 1);
     volatile int* abort_flag = &c->abort_flag;
 
@@ -877,10 +871,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
+        uint8_t* stage = epi + ew * kWEpiBytes;
         Ring acc;
         for (int64_t tile = pair; tile < tiles; tile += pairs) {
             const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
-            const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32 + lane, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
+            const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count[e] > 0;
             if (some) {
                 if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
@@ -893,18 +888,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t base =
                 tmem + acc.s * kAccCols + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
-            T* out = static_cast<T*>(a.out) + ((int64_t)e * a.N + row) * a.K + k0;
+            constexpr int COLS = 128 / (int)sizeof(T);  // of one tile store
 #pragma unroll 1
-            for (int j = 0; j < kWN / 2; j += 32) {
-                float v[32];
-                if (some) {
-                    ptx::tmem_ld32(base + j, v);
-                } else {
+            for (int j = 0; j < kWN / 2; j += COLS) {
+                if (row >= a.N || k0 + j >= a.K) break;
+                float v[COLS];
+                if (!some) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    for (int i = 0; i < COLS; ++i) v[i] = 0.0f;
+                } else if constexpr (COLS == 64) {
+                    ptx::tmem_ld64(base + j, v);
+                } else {
+                    ptx::tmem_ld32(base + j, v);
                 }
-                if (row < a.N) store32(out + j, v, a.K - k0 - j);
+                if (lane == 0) ptx::tma_store_wait_read();
                 __syncwarp();
+                stage_row<T>(stage, v, lane);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::tma_store(&tmOut, ptx::smem_u32(stage), k0 + j, row, e);
             }
             if (some) {
                 ptx::tc_fence_before();
@@ -913,24 +915,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc.step(2);
             }
         }
+        if (lane == 0) ptx::tma_store_wait();
     }
     __syncwarp();
     end_block(tmem, warp);
 }
 
-// Column sums of the segments: a block per (expert, 256 columns), its eight
-// warps over rows in steps of 8, joined in warp order.
+// Column sums of the segments: a cluster of eight blocks per (expert, 256
+// columns), its 64 warps over the rows in turn, joined in warp and block order.
+// (A second pass over grad_out, 75 us of the 960 for 32768 x 7168 rows.
+// Started beside expert_weight_kernel, one block an SM, it made both last
+// 1190 us.)
+constexpr int kBiasBlocks = 8;
+
 __global__ void __launch_bounds__(256)
     expert_bias_kernel(const bf16* dy, const int32_t* off, int64_t P, int N, float* grad_bias) {
     __shared__ float part[8][256];
+    __shared__ float joined[kBiasBlocks][256];  // the first block's is used
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.y, c = blockIdx.x * 256 + lane * 8;
+    const int rank = (int)ptx::cluster_ctarank();
+    const int e = blockIdx.y, c0 = blockIdx.x / kBiasBlocks * 256, c = c0 + lane * 8;
     ptx::griddep_wait();
     const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
     const int64_t lo = b < 0 ? 0 : b > P ? P : b, hi = t > P ? P : t;
     float s[8] = {};
-    if (c < N)
-        for (int64_t r = lo + warp; r < hi; r += 8) {
+    if (c < N) {
+#pragma unroll 4
+        for (int64_t r = lo + rank * 8 + warp; r < hi; r += 8 * kBiasBlocks) {
             const uint4 v = *reinterpret_cast<const uint4*>(dy + r * N + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -940,22 +951,29 @@ __global__ void __launch_bounds__(256)
                 s[2 * i + 1] += f.y;
             }
         }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[warp][lane * 8 + i] = s[i];
     __syncthreads();
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col < N) {
-        float sum = 0.0f;
+    float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) sum += part[w][threadIdx.x];
+    for (int w = 0; w < 8; ++w) sum += part[w][threadIdx.x];
+    ptx::st_cluster_u32(ptx::map_to_rank(ptx::smem_u32(&joined[rank][threadIdx.x]), 0), __float_as_uint(sum));
+    ptx::cluster_sync();
+    const int col = c0 + threadIdx.x;
+    if (rank == 0 && col < N) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kBiasBlocks; ++i) sum += joined[i][threadIdx.x];
         grad_bias[(int64_t)e * N + col] = sum;
     }
 }
 
 // ---------------------------------------------------------------- host
-// A bf16 tensor of `rank` dimensions, innermost first; strides in elements.
+// A bf16 (or fp32) tensor of `rank` dimensions, innermost first; strides in
+// elements; 128 bytes of the innermost to a box.
 cudaError_t encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                   const uint32_t* box) {
+                   const uint32_t* box, bool f32 = false) {
     using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -976,9 +994,9 @@ cudaError_t encode(CUtensorMap* map, const void* base, int rank, const uint64_t*
         d[i] = dims[i];
         b[i] = box[i];
         one[i] = 1;
-        if (i > 0) st[i - 1] = strides[i - 1] * 2;
+        if (i > 0) st[i - 1] = strides[i - 1] * (f32 ? 4 : 2);
     }
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
+    CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -1025,15 +1043,20 @@ int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t s
 
 constexpr size_t kSmemMax = 232448;  // 227 KB
 constexpr size_t kTail = kEpiWarps * kEpiBytes + sizeof(Control) + sizeof(Segments);
-constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + sizeof(Control) + sizeof(Segments);
+constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + kEpiWarps * kWEpiBytes + sizeof(Control) + sizeof(Segments);
 static_assert(kWeightSmem <= kSmemMax, "weight gradient's shared memory");
 static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + kTail <= kSmemMax, "row products' shared memory");
 
-// Tokens per tile, by the experts' mean share of rows: narrow tiles leave
-// room for more stages, which a product that waits for its weights needs.
-void choose_tile(RowArgs& a) {
+// Tokens per tile: enough for the experts' mean share of rows (narrow tiles
+// leave room for more stages, which a product that waits for its weights
+// needs), but no more than lets the tiles reach every pair of SMs: a call of
+// few tiles takes as long as one of them.  (2-slot batch of 3373 tokens, one
+// expert here, 200 x 232 with every part of the epilogue: 9.9 us with tiles of
+// 32, 15.2 with tiles of 256.)
+void choose_tile(RowArgs& a, int pairs) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
+    while (a.tn_max > 32 && (a.P + a.tn_max - 1) / a.tn_max * a.tiles_f < pairs) a.tn_max /= 2;
     a.stage_bytes = kABytes + a.tn_max / 2 * kBK * 2;
     const int fit = (int)((kSmemMax - 1024 - kTail) / a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
@@ -1046,6 +1069,7 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     if (rc != MOE_OK) return rc;
     rc = allow_smem((const void*)expert_rows_kernel<MODE>, dev, kSmemMax);
     if (rc != MOE_OK) return rc;
+    choose_tile(a, sms / 2);
     CUtensorMap tmX, tmX16;  // boxes of 32 and of 16 tokens: a CTA's half of any number of units
     cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, 32);
     if (err == cudaSuccess) err = encode_rows(&tmX16, x, a.P, x_cols, 16);
@@ -1124,7 +1148,6 @@ int moe_expert_matmul(const void* x, const void* weight, const int32_t* expert_o
     a.extra = (const bf16*)residual;
     a.out = (bf16*)out;
     a.preact = (bf16*)preact_out;
-    choose_tile(a);
     CUtensorMap tmW;
     cudaError_t err;
     const uint64_t k = K, n = N;
@@ -1164,7 +1187,6 @@ int moe_expert_matmul_grad_input(const void* grad_out, const void* weight, const
     a.act = activation;
     a.extra = (const bf16*)preact;
     a.out = (bf16*)grad_x;
-    choose_tile(a);
     const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)K, (uint64_t)N * K};
     const uint32_t box[3] = {64, kBK, 1};
     CUtensorMap tmW;
@@ -1190,24 +1212,28 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     int dev = 0, sms = 0;
     int rc2 = sm_count(&dev, &sms);
     if (rc2 != MOE_OK) return rc2;
-    WeightArgs a = {expert_offsets, P, E, N, K, (N + 2 * kM - 1) / (2 * kM), (K + kWN - 1) / kWN, grad_weight, grad_bias};
-    CUtensorMap tmY, tmX;
+    WeightArgs a = {expert_offsets, P, E, N, K, (N + 2 * kM - 1) / (2 * kM), (K + kWN - 1) / kWN};
+    CUtensorMap tmY, tmX, tmOut;
+    const bool f32 = dtype == MOE_DTYPE_F32;
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)K, (uint64_t)N * K};
+    const uint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
     // with P == 0 nothing is read through the maps; they still have to be valid ones
     cudaError_t err = encode_rows(&tmY, P ? grad_out : grad_weight, P ? P : 1, N, kBK);
     if (err == cudaSuccess) err = encode_rows(&tmX, P ? x : grad_weight, P ? P : 1, K, kBK);
-    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
-    if (dtype == MOE_DTYPE_F32) {
+    if (err == cudaSuccess) err = encode(&tmOut, grad_weight, 3, dims, strides, box, f32);
+    if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(grad_weight)");
+    if (f32) {
         rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kWeightSmem);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, tmOut, a);
     } else {
         rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kWeightSmem);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, a);
+            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, tmOut, a);
     }
     if (rc2 != MOE_OK || !grad_bias) return rc2;
-    return launch(expert_bias_kernel, dim3((N + 255) / 256, E), 1, 256, 0, who, stream, (const bf16*)grad_out,
-                  expert_offsets, P, (int)N, grad_bias);
+    return launch(expert_bias_kernel, dim3((N + 255) / 256 * kBiasBlocks, E), kBiasBlocks, 256, 0, who, stream,
+                  (const bf16*)grad_out, expert_offsets, P, (int)N, grad_bias);
 }
 
 }  // extern "C"
