@@ -114,17 +114,17 @@ __device__ __forceinline__ float2 mills(float2 t) {
 // issued instructions, hence two values an instruction wherever there is one
 // for it; the approximate exponential's and reciprocal's few units in the 24th
 // bit vanish in the rounding to bf16.  A NaN stays one.
-template <bool GRAD>
-__device__ __forceinline__ float2 activate(float2 z, int act, float2* slope) {
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float2 activate(float2 z, float2* slope) {
     using namespace ptx;
     constexpr float kLog2e = 1.4426950408889634f;
-    if (act == MOE_ACT_SILU) {
+    if constexpr (ACT == MOE_ACT_SILU) {
         const float2 p = rcp_2(add2(exp2_2(mul2(z, -kLog2e)), both(1.0f)));
         const float2 f = mul2(z, p);
         if (GRAD) *slope = fma2(f, fma2(p, both(-1.0f), 1.0f), p);  // p + z p (1 - p)
         return f;
     }
-    if (act == MOE_ACT_GELU) {
+    if constexpr (ACT == MOE_ACT_GELU) {
         const float2 u = make_float2(fabsf(z.x), fabsf(z.y));
         const float2 t = make_float2(min_nan(u.x, 14.0f), min_nan(u.y, 14.0f));
         const float2 density = mul2(exp2_2(mul2(mul2(t, t), -0.5f * kLog2e)), 0.3989422804014327f);
@@ -370,6 +370,47 @@ __device__ __forceinline__ void prefetch_extra(const RowArgs& a, const Tile& t, 
     }
 }
 
+// f of a fragment's values in place (of the gate's half only unless ALL), in
+// the first `groups` groups of 8 tokens.
+template <int ACT, bool ALL>
+__device__ __forceinline__ void activate_all(float (&acc)[2][4][4], int groups) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i >= groups) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < (ALL ? 4 : 2); p += 2) {
+                const float2 v = activate<ACT, false>(make_float2(acc[h][i][p], acc[h][i][p + 1]), nullptr);
+                acc[h][i][p] = v.x;
+                acc[h][i][p + 1] = v.y;
+            }
+    }
+}
+
+// The fragment q taken on through f at the preactivations g (and, gated, the
+// other factor u): w = q f'(g) [u], u = q f(g).
+template <int ACT, bool GATED>
+__device__ __forceinline__ void through_all(const float (&acc)[2][4][4], const uint32_t (&g)[4][4],
+                                            uint32_t (&u)[4][4], uint32_t (&w)[4][4], int groups) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i >= groups) break;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            float2 q = make_float2(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]), slope;
+            const float2 f = activate<ACT, true>(unpack(g[i][m]), &slope);
+            if constexpr (GATED) {
+                const float2 v = unpack(u[i][m]), other = ptx::mul2(q, f);
+                u[i][m] = pack(other.x, other.y);
+                q = ptx::mul2(q, v);
+            }
+            q = ptx::mul2(q, slope);
+            w[i][m] = pack(q.x, q.y);
+        }
+    }
+}
+
 // One warp's 32 lanes x 32 tokens of the accumulator at taddr.
 template <int MODE>
 __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, const Bias<MODE>& bias, uint32_t taddr,
@@ -419,17 +460,16 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             get32(sst, r, lane);
             __syncwarp();
         }
+        if (a.act == MOE_ACT_SILU) activate_all<MOE_ACT_SILU, true>(acc, groups);
+        else if (a.act == MOE_ACT_GELU) activate_all<MOE_ACT_GELU, true>(acc, groups);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= groups) break;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const float* z = &acc[m / 2][i][2 * (m % 2)];
-                float2 v = activate<false>(make_float2(z[0], z[1]), a.act, nullptr);
+                float2 v = make_float2(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]);
                 if (a.extra != nullptr) v = ptx::add2(v, unpack(r[i][m]));
                 w[i][m] = pack(v.x, v.y);
             }
-        }
         put32(sst, w, lane);
         __syncwarp();
         stage_to_global<64>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
@@ -467,17 +507,16 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
             get16(sst, r, lane);
             __syncwarp();
         }
+        if (a.act == MOE_ACT_SILU) activate_all<MOE_ACT_SILU, false>(acc, groups);
+        else if (a.act == MOE_ACT_GELU) activate_all<MOE_ACT_GELU, false>(acc, groups);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= groups) break;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float2 v = activate<false>(make_float2(acc[h][i][0], acc[h][i][1]), a.act, nullptr);
-                v = ptx::mul2(v, make_float2(acc[h][i][2], acc[h][i][3]));
+                float2 v = ptx::mul2(make_float2(acc[h][i][0], acc[h][i][1]), make_float2(acc[h][i][2], acc[h][i][3]));
                 if (a.extra != nullptr) v = ptx::add2(v, unpack(r[i][h]));
                 w[i][h] = pack(v.x, v.y);
             }
-        }
         put16(sst, w, lane);
         __syncwarp();
         stage_to_global<32>(stage, a.out + row0 * a.N + col0, a.N, valid, cols, lane);
@@ -495,24 +534,18 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
                 __syncwarp();
             }
         }
+        if (a.extra == nullptr) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= groups) break;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                float2 q = make_float2(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]);
-                if (a.extra != nullptr) {
-                    float2 slope;
-                    const float2 f = activate<true>(unpack(g[i][m]), a.act, &slope);
-                    if constexpr (MODE == kGradGated) {
-                        const float2 v = unpack(u[i][m]), other = ptx::mul2(q, f);
-                        u[i][m] = pack(other.x, other.y);
-                        q = ptx::mul2(q, v);
-                    }
-                    q = ptx::mul2(q, slope);
-                }
-                w[i][m] = pack(q.x, q.y);
-            }
+                for (int m = 0; m < 4; ++m)
+                    w[i][m] = pack(acc[m / 2][i][2 * (m % 2)], acc[m / 2][i][2 * (m % 2) + 1]);
+        } else if (a.act == MOE_ACT_SILU) {
+            through_all<MOE_ACT_SILU, MODE == kGradGated>(acc, g, u, w, groups);
+        } else if (a.act == MOE_ACT_GELU) {
+            through_all<MOE_ACT_GELU, MODE == kGradGated>(acc, g, u, w, groups);
+        } else {
+            through_all<MOE_ACT_NONE, MODE == kGradGated>(acc, g, u, w, groups);
         }
         put32(sst, w, lane);
         __syncwarp();
@@ -706,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 epilogue_chunk<MODE>(a, t, bias, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
+            if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
         }
     }
     __syncwarp();
@@ -911,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (some) {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
+                if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
                 acc.step(2);
             }
         }

@@ -157,6 +157,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t& a, u
                  : "memory");
 }
 
+// Arrive on an mbarrier of another CTA of the cluster, ordering this thread's
+// own CTA only.  For hand-overs of TMEM, which tcgen05 fences order: a release
+// at cluster scope would wait for every global store the thread has made.
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // ---------------------------------------------------------------- pairs of floats
 // Two fp32 operations per instruction.
 __device__ __forceinline__ unsigned long long pair_of(float2 v) {
