@@ -74,7 +74,7 @@ struct RowArgs {
     int64_t P;
     int E;
     int red;             // reduction length
-    int tiles_f;         // pairs of feature tiles
+    unsigned tiles_f;    // pairs of feature tiles
     int tn_max;          // tokens per tile at most
     int stages, stage_bytes;
     int N;               // columns of one output part
@@ -89,7 +89,7 @@ struct WeightArgs {
     const int32_t* off;
     int64_t P;
     int E, N, K;
-    int tiles_n, tiles_k;  // of 256 x 256
+    unsigned tiles_n, tiles_k;  // of 256 x 256
 };
 
 // The normal distribution's tail over its density at t >= 0 (Mills' ratio),
@@ -187,6 +187,14 @@ __device__ __forceinline__ void give_up(volatile int* abort_flag) {
     atomicAdd(&g_watchdog_trips_experts, 1u);
 }
 
+// Gives the copies that a lane has issued time to land before it leaves after
+// a wait that ran out (a millisecond; a copy takes a few microseconds).  Where
+// all goes well they have landed when the last accumulator is complete.
+__device__ __forceinline__ void settle() {
+    const uint64_t until = ptx::globaltimer_ns() + 1000000;
+    while (ptx::globaltimer_ns() < until) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------- segments
 // begin[e] and cum[e]: first row of expert e, and token tiles of the experts
 // before it.
@@ -200,10 +208,27 @@ __device__ __forceinline__ int tiles_of(int count, int tn_max) {
     return (int)(((unsigned)count + tn_max - 1) / (unsigned)tn_max);
 }
 
+// The offsets of this thread's experts, read ahead of the barriers of
+// start_block.
+struct Offsets {
+    int32_t at[(kMaxE + kThreads - 1) / kThreads][2];
+    __device__ __forceinline__ void load(const int32_t* off, int E) {
+#pragma unroll
+        for (int i = 0; i < (kMaxE + kThreads - 1) / kThreads; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            at[i][0] = e < E ? __ldg(off + e) : 0;
+            at[i][1] = e < E ? __ldg(off + e + 1) : 0;
+        }
+    }
+};
+
 // All threads of the block; ends with a barrier.
-__device__ void load_segments(Segments& s, const int32_t* off, int E, int64_t P, int tn_max) {
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-        const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
+__device__ void load_segments(Segments& s, const Offsets& off, int E, int64_t P, int tn_max) {
+#pragma unroll
+    for (int i = 0; i < (kMaxE + kThreads - 1) / kThreads; ++i) {
+        const int e = threadIdx.x + i * kThreads;
+        if (e >= E) break;
+        const int64_t b = off.at[i][0], t = off.at[i][1];
         const int64_t lo = b < 0 ? 0 : b > P ? P : b;
         const int64_t hi = t > P ? P : t;
         s.begin[e] = (int)lo;
@@ -225,9 +250,9 @@ __device__ void load_segments(Segments& s, const int32_t* off, int E, int64_t P,
             s.cum[e] = at;
             at += tiles_of(s.count[e], tn_max);
         }
-        // Ranges that overlap so often that their tiles pass 32 bits are no
-        // permutation's: no tile at all.
-        if (threadIdx.x == 31) s.cum[E] = incl >> 31 ? 0u : (unsigned)incl;
+        // More tiles than P rows in E segments can have: the ranges overlap,
+        // which is no permutation's doing.  No tile at all.
+        if (threadIdx.x == 31) s.cum[E] = incl > (unsigned long long)(P / tn_max + E) ? 0u : (unsigned)incl;
     }
     __syncthreads();
 }
@@ -242,22 +267,22 @@ struct Tile {
 
 // Tiles run over experts, then feature tiles, then the token tiles of the
 // expert, so that neighbouring blocks share the weight's rows.
-__device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, int64_t tile, int rank) {
+__device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, unsigned tile, int rank) {
     int lo = 0, hi = a.E;  // cum[lo] * tiles_f <= tile < cum[hi] * tiles_f
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)s.cum[mid] * a.tiles_f <= tile) lo = mid;
+        if (s.cum[mid] * a.tiles_f <= tile) lo = mid;
         else hi = mid;
     }
     Tile t;
     t.e = lo;
-    const int parts = tiles_of(s.count[lo], a.tn_max);
-    const int64_t in = tile - (int64_t)s.cum[lo] * a.tiles_f;
-    const int f_pair = (int)(in / parts);
+    const unsigned parts = tiles_of(s.count[lo], a.tn_max);
+    const unsigned in = tile - s.cum[lo] * a.tiles_f;
+    const int f_pair = in / parts;
     t.f = 2 * f_pair + rank;
-    const int part = (int)(in - (int64_t)f_pair * parts);
+    const int part = in - f_pair * parts;
     // equal parts to within one unit of 32 tokens
-    const int units = (s.count[lo] + kUnit - 1) / kUnit, q = units / parts, more = units - q * parts;
+    const int units = (s.count[lo] + kUnit - 1) / kUnit, q = (unsigned)units / parts, more = units - q * (int)parts;
     const int first = part * q + (part < more ? part : more);
     t.row0 = s.begin[lo] + first * kUnit;
     t.tn = (q + (part < more ? 1 : 0)) * kUnit;
@@ -574,26 +599,26 @@ struct Control {
 
 // Barriers, TMEM and the meeting of the pair's two CTAs.
 __device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp) {
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            ptx::mbar_init(&c->full[s], 1);
-            ptx::mbar_init(&c->tail[s], 1);
-            ptx::mbar_init(&c->cut[s], 2);
-            ptx::mbar_init(&c->empty[s], 1);
+    if (warp == 0) {
+        const int lane = threadIdx.x;
+        if (lane < stages) {
+            ptx::mbar_init(&c->full[lane], 1);
+            ptx::mbar_init(&c->tail[lane], 1);
+            ptx::mbar_init(&c->cut[lane], 2);
+            ptx::mbar_init(&c->empty[lane], 1);
+        } else if (lane >= 30) {
+            ptx::mbar_init(&c->acc_full[lane - 30], 1);
+            ptx::mbar_init(&c->acc_empty[lane - 30], 2 * kEpiWarps);
+            c->abort_flag = 0;
         }
-        for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&c->acc_full[b], 1);
-            ptx::mbar_init(&c->acc_empty[b], 2 * kEpiWarps);
-        }
-        c->abort_flag = 0;
         ptx::fence_mbar_init();
+        __syncwarp();
     }
     if (warp == 2) {
         ptx::tmem_alloc_pair(&c->tmem, 2 * kAccCols);
         ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
-    __syncthreads();
     ptx::cluster_sync();
     ptx::tc_fence_after();
     return c->tmem;
@@ -603,7 +628,6 @@ __device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp
 // memory and arrives on its barriers.
 __device__ __forceinline__ void end_block(uint32_t tmem, int warp) {
     ptx::tc_fence_before();
-    __syncthreads();
     ptx::cluster_sync();
     if (warp == 2) {
         ptx::tc_fence_after();
@@ -624,16 +648,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1;
+    const unsigned pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmW);
         ptx::tma_prefetch_desc(&tmX);
         ptx::tma_prefetch_desc(&tmX16);
     }
-    const uint32_t tmem = start_block(c, a.stages, warp);
+    // (Nothing of this fits on an SM beside another such block, so there is no
+    // set-up to overlap with the previous kernel.)
     ptx::griddep_wait();
-    load_segments(seg, a.off, a.E, a.P, a.tn_max);
-    const int64_t tiles = (int64_t)seg.cum[a.E] * a.tiles_f;
+    Offsets offsets;
+    offsets.load(a.off, a.E);
+    const uint32_t tmem = start_block(c, a.stages, warp);
+    load_segments(seg, offsets, a.E, a.P, a.tn_max);
+    const unsigned tiles = seg.cum[a.E] * a.tiles_f;
 
     const uint32_t ring_at = ptx::smem_u32(ring), all = a.stages * a.stage_bytes;
     const uint32_t full = ptx::smem_u32(c->full), empty = ptx::smem_u32(c->empty);
@@ -643,18 +672,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // it some 80 cycles to issue.
         if (elect_one()) {
             Stages r;
-            bool ok = true;
+            bool ok = true, ready = true;  // ready: the stage at r is known to be empty
             const uint32_t full_pair = ptx::map_to_rank(full, 0);
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+            for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
                 const Tile t = tile_at(seg, a, tile, rank);
                 const int row0 = t.row0 + rank * (t.tn / 2);  // this CTA's half of the tokens
                 const uint32_t bytes = 2 * kABytes + t.tn * (kBK * 2);
-                for (int k = 0; k < a.red; k += kBK, r.step(a.stage_bytes, all)) {
-                    if (!ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
+                for (int k = 0; k < a.red; k += kBK) {
+                    if (!ready && !ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
+                    Stages next = r;
+                    next.step(a.stage_bytes, all);
+                    ready = ptx::bar_try(empty + next.bar, next.phase ^ 1);
                     const uint32_t at = ring_at + r.at, bar = full_pair + r.bar;
                     if (warp == 0) {
                         // Only the even CTA arrives: its barrier cannot complete
@@ -678,22 +710,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ptx::tma_load(to, &tmX, k, row, bar);
                         if (t.tn & 32) ptx::tma_load(to, &tmX16, k, row, bar);
                     }
+                    r = next;
                 }
             }
-            // Leave only once every stage filled has been used, or its wait has run out.
-            for (int i = 0; i < a.stages; ++i, r.step(a.stage_bytes, all))
-                ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs);
+            if (!ok) settle();
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             Stages r;
             Ring acc;
-            bool ok = true;
+            bool ok = true, ready = false;  // ready: the stage at r is known to be full
             // descriptors of the first stage's operands; steps of 16 in the reduction
             const uint64_t ad0 = GRAD ? ptx::sdesc_sw128(ring_at, kABytes / 2, 1024) : ptx::sdesc_sw128(ring_at, 16, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 16, 1024);
             constexpr uint64_t A_STEP = GRAD ? 2048 >> 4 : 32 >> 4, B_STEP = 32 >> 4;
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs, acc.step(2)) {
+            for (unsigned tile = pair; tile < tiles && ok; tile += pairs, acc.step(2)) {
                 const Tile t = tile_at(seg, a, tile, rank);
                 const uint32_t idesc = ptx::idesc_bf16_m256(t.tn, GRAD, false);
                 if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
@@ -702,18 +733,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
-                for (int k = 0; k < a.red; k += kBK, r.step(a.stage_bytes, all)) {
-                    if (!ptx::bar_wait<true>(full + r.bar, r.phase, kWaitNs)) {
+                for (int k = 0; k < a.red; k += kBK) {
+                    if (!ready && !ptx::bar_wait<true>(full + r.bar, r.phase, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
+                    // a look at the next stage's barrier takes as long as two
+                    // narrow products to come back
+                    Stages next = r;
+                    next.step(a.stage_bytes, all);
+                    ready = ptx::bar_try_cluster(full + next.bar, next.phase);
                     ptx::tc_fence_after();
                     const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         ptx::umma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, (k | kk) != 0);
                     ptx::umma_commit_pair(empty + r.bar);
+                    r = next;
                 }
                 ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]));
             }
@@ -722,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         uint8_t* stage = epi + ew * kEpiBytes;
         Ring acc;
-        for (int64_t tile = pair; tile < tiles; tile += pairs, acc.step(2)) {
+        for (unsigned tile = pair; tile < tiles; tile += pairs, acc.step(2)) {
             const Tile t = tile_at(seg, a, tile, rank);
             Bias<MODE> bias;
             bias.load(a, t, quarter, lane);
@@ -785,16 +822,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1;
+    const unsigned pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmY);
         ptx::tma_prefetch_desc(&tmX);
     }
-    const uint32_t tmem = start_block(c, kWStages, warp);
     ptx::griddep_wait();
-    load_segments(seg, a.off, a.E, a.P, kBK);
-    const int per_e = a.tiles_n * a.tiles_k;
-    const int64_t tiles = (int64_t)a.E * per_e;
+    Offsets offsets;
+    offsets.load(a.off, a.E);
+    const uint32_t tmem = start_block(c, kWStages, warp);
+    load_segments(seg, offsets, a.E, a.P, kBK);
+    const unsigned per_e = a.tiles_n * a.tiles_k, tiles = a.E * per_e;
 
     const uint32_t ring_at = ptx::smem_u32(ring);
     const uint32_t full = ptx::smem_u32(c->full), tail = ptx::smem_u32(c->tail), cut = ptx::smem_u32(c->cut),
@@ -808,8 +847,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t full_pair = ptx::map_to_rank(full, 0);
             const CUtensorMap* tm = warp == 0 ? &tmY : &tmX;
             const uint32_t part = ring_at + (warp == 0 ? 0 : kABytes);
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
-                const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
+            for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
+                const int e = tile / per_e;
+                const unsigned in = tile - e * per_e;
                 const int c0 = warp == 0 ? (in / a.tiles_k * 2 + rank) * kM : in % a.tiles_k * kWN + rank * (kWN / 2);
                 const int count = seg.count[e], row0 = seg.begin[e];
                 for (int p = 0; p < count; p += kBK, r.step(kWStageBytes, all)) {
@@ -830,8 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tma_load(part + r.at + 8192, tm, c0 + 64, row0 + p, bar);
                 }
             }
-            for (int i = 0; i < kWStages; ++i, r.step(kWStageBytes, all))
-                ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs);
+            if (!ok) settle();
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -842,8 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const uint64_t ad0 = ptx::sdesc_sw128(ring_at, 8192, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 8192, 1024);
-            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
-                const int count = seg.count[(int)(tile / per_e)];
+            for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
+                const int count = seg.count[tile / per_e];
                 if (count == 0) continue;
                 if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
                     give_up(abort_flag);
@@ -881,8 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Stages r;
         uint32_t uses = 0;  // parity of each stage's uses as a tail
         bool ok = true;
-        for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
-            const int count = seg.count[(int)(tile / per_e)], left = count % kBK;
+        for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
+            const int count = seg.count[tile / per_e], left = count % kBK;
             for (int p = kBK; p <= count; p += kBK) r.step(kWStageBytes, all);
             if (left == 0) continue;
             const uint32_t bit = r.bar >> 3;
@@ -906,8 +945,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         uint8_t* stage = epi + ew * kWEpiBytes;
         Ring acc;
-        for (int64_t tile = pair; tile < tiles; tile += pairs) {
-            const int e = (int)(tile / per_e), in = (int)(tile - (int64_t)e * per_e);
+        for (unsigned tile = pair; tile < tiles; tile += pairs) {
+            const int e = tile / per_e;
+                const unsigned in = tile - e * per_e;
             const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count[e] > 0;
             if (some) {
@@ -1074,6 +1114,8 @@ int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t s
     return err == cudaSuccess ? MOE_OK : set_cuda_error(err, who);
 }
 
+int check_tiles(const char* who, int64_t tiles);
+
 constexpr size_t kSmemMax = 232448;  // 227 KB
 constexpr size_t kTail = kEpiWarps * kEpiBytes + sizeof(Control) + sizeof(Segments);
 constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + kEpiWarps * kWEpiBytes + sizeof(Control) + sizeof(Segments);
@@ -1103,6 +1145,8 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     rc = allow_smem((const void*)expert_rows_kernel<MODE>, dev, kSmemMax);
     if (rc != MOE_OK) return rc;
     choose_tile(a, sms / 2);
+    rc = check_tiles(who, (a.P / a.tn_max + a.E) * a.tiles_f);
+    if (rc != MOE_OK) return rc;
     CUtensorMap tmX, tmX16;  // boxes of 32 and of 16 tokens: a CTA's half of any number of units
     cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, 32);
     if (err == cudaSuccess) err = encode_rows(&tmX16, x, a.P, x_cols, 16);
@@ -1136,6 +1180,14 @@ int check_sizes(const char* who, int64_t P, int K, int N, int E, int activation,
         return set_error(MOE_ERR_UNSUPPORTED, msg);
     }
     return MOE_OK;
+}
+
+// Tiles are counted in 32 bits.
+int check_tiles(const char* who, int64_t tiles) {
+    if (tiles < (1ll << 31)) return MOE_OK;
+    char msg[256];
+    snprintf(msg, sizeof msg, "%s: %lld tiles of work are too many for one call", who, (long long)tiles);
+    return set_error(MOE_ERR_UNSUPPORTED, msg);
 }
 
 int bad_pointer(const char* who) {
@@ -1245,7 +1297,9 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     int dev = 0, sms = 0;
     int rc2 = sm_count(&dev, &sms);
     if (rc2 != MOE_OK) return rc2;
-    WeightArgs a = {expert_offsets, P, E, N, K, (N + 2 * kM - 1) / (2 * kM), (K + kWN - 1) / kWN};
+    WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM), (unsigned)(K + kWN - 1) / kWN};
+    rc2 = check_tiles(who, (int64_t)a.E * a.tiles_n * a.tiles_k);
+    if (rc2 != MOE_OK) return rc2;
     CUtensorMap tmY, tmX, tmOut;
     const bool f32 = dtype == MOE_DTYPE_F32;
     const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E}, strides[2] = {(uint64_t)K, (uint64_t)N * K};
