@@ -63,6 +63,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kPitch = 80;              // bytes of a staged token: 32 features and a bank shift
 constexpr int kEpiBytes = 32 * kPitch;  // per epilogue warp: 32 tokens
+constexpr int kSumBytes = kM * 32 * 4;  // a CTA's fp32 sums of a 32-token tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 static __device__ unsigned int g_watchdog_trips_experts;
@@ -77,6 +78,7 @@ struct RowArgs {
     unsigned tiles_f;    // pairs of feature tiles
     int tn_max;          // tokens per tile at most
     int stages, stage_bytes;
+    int split;           // pairs of a cluster that share a tile's reduction
     int N;               // columns of one output part
     const float* bias;   // (E, N) or (E, 2 N)
     int act;
@@ -252,7 +254,7 @@ __device__ void load_segments(Segments& s, const Offsets& off, int E, int64_t P,
         }
         // More tiles than P rows in E segments can have: the ranges overlap,
         // which is no permutation's doing.  No tile at all.
-        if (threadIdx.x == 31) s.cum[E] = incl > (unsigned long long)(P / tn_max + E) ? 0u : (unsigned)incl;
+        if (threadIdx.x == 31) s.cum[E] = incl > (unsigned long long)(P / tn_max + (E < P ? E : P)) ? 0u : (unsigned)incl;
     }
     __syncthreads();
 }
@@ -436,6 +438,39 @@ __device__ __forceinline__ void through_all(const float (&acc)[2][4][4], const u
     }
 }
 
+// Split reductions: a warp's fragment to the first pair's CTA of the same rank
+// (piece i of thread l at 16 (32 i + l)), and there on top of its own.
+__device__ __forceinline__ void send_sums(uint32_t taddr, uint32_t sums, uint32_t joined, int rank, int quarter,
+                                          int lane) {
+    float acc[2][4][4];
+    ptx::tmem_ld_frag32(taddr, acc);
+    const uint32_t to = ptx::map_to_rank(sums + quarter * (kSumBytes / 4) + lane * 16, rank);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float* v = acc[i / 4][i % 4];
+        ptx::st_cluster_f32x4(to + i * 512, v[0], v[1], v[2], v[3]);
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(joined, rank));
+}
+__device__ __forceinline__ void add_sums(uint32_t taddr, const uint8_t* sums, int parts, int quarter, int lane) {
+    float acc[2][4][4];
+    ptx::tmem_ld_frag32(taddr, acc);
+    for (int part = 0; part < parts; ++part) {
+        const float4* from = reinterpret_cast<const float4*>(sums + part * kSumBytes + quarter * (kSumBytes / 4)) + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 v = from[i * 32];
+            float* to = acc[i / 4][i % 4];
+            to[0] += v.x;
+            to[1] += v.y;
+            to[2] += v.z;
+            to[3] += v.w;
+        }
+    }
+    ptx::tmem_st_frag32(taddr, acc);
+}
+
 // One warp's 32 lanes x 32 tokens of the accumulator at taddr.
 template <int MODE>
 __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, const Bias<MODE>& bias, uint32_t taddr,
@@ -593,12 +628,13 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
 // has been read.
 struct Control {
     uint64_t full[kMaxStages], tail[kMaxStages], cut[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint64_t joined;     // split reductions: the other pairs' sums are here
     uint32_t tmem;
     int abort_flag;
 };
 
 // Barriers, TMEM and the meeting of the pair's two CTAs.
-__device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp) {
+__device__ __forceinline__ uint32_t start_block(Control* c, int stages, int split, int warp) {
     if (warp == 0) {
         const int lane = threadIdx.x;
         if (lane < stages) {
@@ -609,6 +645,7 @@ __device__ __forceinline__ uint32_t start_block(Control* c, int stages, int warp
         } else if (lane >= 30) {
             ptx::mbar_init(&c->acc_full[lane - 30], 1);
             ptx::mbar_init(&c->acc_empty[lane - 30], 2 * kEpiWarps);
+            if (lane == 30) ptx::mbar_init(&c->joined, 4 * (split > 1 ? split - 1 : 1));
             c->abort_flag = 0;
         }
         ptx::fence_mbar_init();
@@ -643,13 +680,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = ptx::smem_align<1024>(smem_raw);
     uint8_t* epi = ring + a.stages * a.stage_bytes;
-    Control* c = reinterpret_cast<Control*>(epi + kEpiWarps * kEpiBytes);
+    uint8_t* sums = epi + kEpiWarps * kEpiBytes;  // split reductions: the other pairs' parts
+    Control* c = reinterpret_cast<Control*>(sums + (a.split - 1) * kSumBytes);
     Segments& seg = *reinterpret_cast<Segments*>(c + 1);
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1;
-    const unsigned pairs = gridDim.x >> 1;
+    // A cluster of `split` pairs has a tile at a time; `slice` is this pair's
+    // part of the reduction, `lead` its even CTA.
+    const int cta = (int)ptx::cluster_ctarank(), rank = cta & 1, lead = cta & ~1, slice = cta >> 1;
+    const unsigned pair = blockIdx.x / (2 * a.split), pairs = gridDim.x / (2 * a.split);
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmW);
         ptx::tma_prefetch_desc(&tmX);
@@ -660,12 +700,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::griddep_wait();
     Offsets offsets;
     offsets.load(a.off, a.E);
-    const uint32_t tmem = start_block(c, a.stages, warp);
+    const uint32_t tmem = start_block(c, a.stages, a.split, warp);
     load_segments(seg, offsets, a.E, a.P, a.tn_max);
     const unsigned tiles = seg.cum[a.E] * a.tiles_f;
 
     const uint32_t ring_at = ptx::smem_u32(ring), all = a.stages * a.stage_bytes;
     const uint32_t full = ptx::smem_u32(c->full), empty = ptx::smem_u32(c->empty);
+    const int blocks_k = (a.red + kBK - 1) / kBK;  // this pair's: [k_lo, k_hi)
+    const int k_lo = blocks_k * slice / a.split * kBK, k_hi = blocks_k * (slice + 1) / a.split * kBK;
     if (warp == 0 || warp == 3) {
         // Producers: warp 0 copies the weight's tile, warp 3 the tokens', both
         // to the even CTA's barrier.  One lane for both is late: a copy takes
@@ -673,12 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             Stages r;
             bool ok = true, ready = true;  // ready: the stage at r is known to be empty
-            const uint32_t full_pair = ptx::map_to_rank(full, 0);
+            const uint32_t full_pair = ptx::map_to_rank(full, lead);
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
                 const Tile t = tile_at(seg, a, tile, rank);
                 const int row0 = t.row0 + rank * (t.tn / 2);  // this CTA's half of the tokens
                 const uint32_t bytes = 2 * kABytes + t.tn * (kBK * 2);
-                for (int k = 0; k < a.red; k += kBK) {
+                for (int k = k_lo; k < k_hi; k += kBK) {
                     if (!ready && !ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
@@ -723,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // descriptors of the first stage's operands; steps of 16 in the reduction
             const uint64_t ad0 = GRAD ? ptx::sdesc_sw128(ring_at, kABytes / 2, 1024) : ptx::sdesc_sw128(ring_at, 16, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 16, 1024);
+            const uint16_t ctas = (uint16_t)(3u << lead);
             constexpr uint64_t A_STEP = GRAD ? 2048 >> 4 : 32 >> 4, B_STEP = 32 >> 4;
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs, acc.step(2)) {
                 const Tile t = tile_at(seg, a, tile, rank);
@@ -733,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
-                for (int k = 0; k < a.red; k += kBK) {
+                for (int k = k_lo; k < k_hi; k += kBK) {
                     if (!ready && !ptx::bar_wait<true>(full + r.bar, r.phase, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
@@ -748,11 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        ptx::umma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, (k | kk) != 0);
-                    ptx::umma_commit_pair(empty + r.bar);
+                        ptx::umma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, k != k_lo || kk != 0);
+                    ptx::umma_commit_pair(empty + r.bar, ctas);
                     r = next;
                 }
-                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]));
+                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), ctas);
             }
         }
     } else if (warp >= 4) {
@@ -772,11 +815,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*abort_flag) break;
             ptx::tc_fence_after();
             const uint32_t base = tmem + acc.s * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int tok0 = half * 32; tok0 < t.valid; tok0 += 64)
+            if (a.split > 1 && half == 0) {
+                // one chunk of 32 tokens; its sums meet in the first pair
+                if (slice > 0) {
+                    send_sums(base, ptx::smem_u32(sums) + (slice - 1) * kSumBytes, ptx::smem_u32(&c->joined), rank,
+                              quarter, lane);
+                } else if (ptx::mbar_wait_cluster(&c->joined, 0, kWaitNs)) {
+                    __syncwarp();
+                    add_sums(base, sums, a.split - 1, quarter, lane);
+                } else {
+                    if (lane == 0) give_up(abort_flag);
+                    *abort_flag = 1;
+                }
+                __syncwarp();
+                if (*abort_flag) break;
+            }
+            for (int tok0 = half * 32; tok0 < t.valid && slice == 0; tok0 += 64)
                 epilogue_chunk<MODE>(a, t, bias, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
+            if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), lead));
         }
     }
     __syncwarp();
@@ -822,8 +880,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)ptx::cluster_ctarank(), pair = blockIdx.x >> 1;
-    const unsigned pairs = gridDim.x >> 1;
+    const int rank = (int)ptx::cluster_ctarank();
+    const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         ptx::tma_prefetch_desc(&tmY);
         ptx::tma_prefetch_desc(&tmX);
@@ -831,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::griddep_wait();
     Offsets offsets;
     offsets.load(a.off, a.E);
-    const uint32_t tmem = start_block(c, kWStages, warp);
+    const uint32_t tmem = start_block(c, kWStages, 1, warp);
     load_segments(seg, offsets, a.E, a.P, kBK);
     const unsigned per_e = a.tiles_n * a.tiles_k, tiles = a.E * per_e;
 
@@ -908,9 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         if (kk < steps)
                             ptx::umma_bf16_pair(d, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), idesc, (p | kk) != 0);
-                    ptx::umma_commit_pair(empty + r.bar);
+                    ptx::umma_commit_pair(empty + r.bar, 3);
                 }
-                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]));
+                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), 3);
                 acc.step(2);
             }
         }
@@ -1128,13 +1186,51 @@ static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + kTail <= kSmemMax, "row pro
 // few tiles takes as long as one of them.  (2-slot batch of 3373 tokens, one
 // expert here, 200 x 232 with every part of the epilogue: 9.9 us with tiles of
 // 32, 15.2 with tiles of 256.)
-void choose_tile(RowArgs& a, int pairs) {
+void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
     while (a.tn_max > 32 && (a.P + a.tn_max - 1) / a.tn_max * a.tiles_f < pairs) a.tn_max /= 2;
+    // Where even tiles of 32 leave most SMs idle, 2 or 4 pairs share a tile's
+    // reduction: a tile's time is then its weight's rows through one pair's
+    // L2 ports (46 bytes a cycle and SM).  One token, 2 of 8 experts, 1024 by
+    // 2 x 512: 7.4 us with four pairs, 8.1 with one; 16 rows of 20 experts,
+    // 1888 by 248: 10.7 and 12.9.  Only where all clusters run at once, so that
+    // each has at most one tile, whose sums need no second buffer.
+    a.split = 1;
+    const int64_t most = (a.P / a.tn_max + (a.E < a.P ? a.E : a.P)) * a.tiles_f, blocks_k = (a.red + kBK - 1) / kBK;
+    if (a.tn_max == 32 && most <= fit2)
+        a.split = most <= fit4 && blocks_k >= 8 ? 4 : blocks_k >= 4 ? 2 : 1;
     a.stage_bytes = kABytes + a.tn_max / 2 * kBK * 2;
-    const int fit = (int)((kSmemMax - 1024 - kTail) / a.stage_bytes);
+    const int fit = (int)((kSmemMax - 1024 - kTail - (a.split - 1) * kSumBytes) / a.stage_bytes);
     a.stages = fit < kMaxStages ? fit : kMaxStages;
+}
+
+// Clusters of `split` pairs that run at once on the current device, looked up
+// once (all forms of the kernel have a block to an SM).
+int clusters_at_once(int dev, int split) {
+    static std::mutex mu;
+    static std::unordered_map<int, int> known;
+    std::lock_guard<std::mutex> lk(mu);
+    auto hit = known.find(dev * 8 + split);
+    if (hit != known.end()) return hit->second;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, expert_rows_kernel<kFwd>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[dev * 8 + split] = n;
+    return n;
 }
 
 template <int MODE>
@@ -1144,15 +1240,19 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     if (rc != MOE_OK) return rc;
     rc = allow_smem((const void*)expert_rows_kernel<MODE>, dev, kSmemMax);
     if (rc != MOE_OK) return rc;
-    choose_tile(a, sms / 2);
+    rc = allow_smem((const void*)expert_rows_kernel<kFwd>, dev, kSmemMax);
+    if (rc != MOE_OK) return rc;
+    const int fit2 = clusters_at_once(dev, 2), fit4 = clusters_at_once(dev, 4);
+    choose_tile(a, sms / 2, fit2, fit4);
     rc = check_tiles(who, (a.P / a.tn_max + a.E) * a.tiles_f);
     if (rc != MOE_OK) return rc;
     CUtensorMap tmX, tmX16;  // boxes of 32 and of 16 tokens: a CTA's half of any number of units
     cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, 32);
     if (err == cudaSuccess) err = encode_rows(&tmX16, x, a.P, x_cols, 16);
     if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
-    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kTail;
-    return launch(expert_rows_kernel<MODE>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmW, tmX, tmX16, a);
+    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + (a.split - 1) * kSumBytes + kTail;
+    const int blocks = a.split == 4 ? fit4 * 8 : a.split == 2 ? fit2 * 4 : sms & ~1;
+    return launch(expert_rows_kernel<MODE>, dim3(blocks), 2 * a.split, kThreads, smem, who, stream, tmW, tmX, tmX16, a);
 }
 
 bool bad(const void* p, size_t n) { return !p || reinterpret_cast<uintptr_t>(p) % n != 0; }

@@ -101,13 +101,13 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
         : "memory");
 }
 
-// Arrive on the mbarrier at this offset in both CTAs of the pair once every
-// product issued so far by this thread is done.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+// Arrive on the mbarrier at this offset in both CTAs of the pair, whose bits
+// are set in `ctas`, once every product issued so far by this thread is done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t ctas) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             bar),
-        "h"((uint16_t)3)
+        "h"(ctas)
         : "memory");
 }
 
@@ -139,6 +139,23 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, float (&v)[2][4][
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i / 16][i / 4 % 4][i % 4] = __uint_as_float(r[i]);
+}
+
+// The same fragment back to TMEM.
+__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const float (&v)[2][4][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[h][i / 4][i % 4]);
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+            "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr + h * (16u << 16)),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+            "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Four 8x8 matrices of 16-bit values between registers (thread l holds row
