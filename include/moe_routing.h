@@ -393,8 +393,9 @@ MOE_API int moe_sort_topk_by_id(float* topk_weights, int32_t* topk_ids, int64_t 
  *     read the same way.)
  *   - Rows at and behind expert_offsets[E] belong to no expert: those of an
  *     output are left as they were, those of an input have no effect,
- *     whatever they hold.  Offsets are read as if clamped to [0, P]; an
- *     expert whose end is not above its start has no rows.
+ *     whatever they hold.  expert_offsets are nondecreasing values in [0, P],
+ *     as moe_expert_permutation writes them; with others the results are
+ *     unspecified, but nothing outside the tensors is touched.
  *   - Row types are MOE_DTYPE_F32 or MOE_DTYPE_BF16; sums are fp32, rounded
  *     once when they are stored.  Results do not depend on timing: the same
  *     inputs give the same bits.

@@ -92,6 +92,7 @@ struct WeightArgs {
     int64_t P;
     int E, N, K;
     unsigned tiles_n, tiles_k;  // of 256 x 256
+    int stages;
 };
 
 // The normal distribution's tail over its density at t >= 0 (Mills' ratio),
@@ -198,63 +199,68 @@ __device__ __forceinline__ void settle() {
 }
 
 // ---------------------------------------------------------------- segments
-// begin[e] and cum[e]: first row of expert e, and token tiles of the experts
-// before it.
+// begin[e] to begin[e + 1] are the rows of expert e; cum[e] counts the token
+// tiles of the experts before it.  Offsets are clamped to [0, P] and made
+// nondecreasing: whatever they hold, segments lie apart and inside the rows.
 struct Segments {
-    int begin[kMaxE];
-    int count[kMaxE];
-    unsigned cum[kMaxE + 1];
+    int* begin;     // E + 1
+    unsigned* cum;  // E + 1
+    __device__ __forceinline__ int count(int e) const { return begin[e + 1] - begin[e]; }
 };
+constexpr size_t segment_bytes(int E) { return (size_t)(E + 1) * 8; }
 
-__device__ __forceinline__ int tiles_of(int count, int tn_max) {
-    return (int)(((unsigned)count + tn_max - 1) / (unsigned)tn_max);
+__device__ __forceinline__ unsigned tiles_of(int count, int tn_max) {
+    return ((unsigned)count + tn_max - 1) / (unsigned)tn_max;
 }
 
-// The offsets of this thread's experts, read ahead of the barriers of
-// start_block.
+// This thread's offsets, read ahead of the barriers of start_block.
 struct Offsets {
-    int32_t at[(kMaxE + kThreads - 1) / kThreads][2];
+    static constexpr int N = (kMaxE + 1 + kThreads - 1) / kThreads;
+    int32_t at[N];
     __device__ __forceinline__ void load(const int32_t* off, int E) {
 #pragma unroll
-        for (int i = 0; i < (kMaxE + kThreads - 1) / kThreads; ++i) {
+        for (int i = 0; i < N; ++i) {
             const int e = threadIdx.x + i * kThreads;
-            at[i][0] = e < E ? __ldg(off + e) : 0;
-            at[i][1] = e < E ? __ldg(off + e + 1) : 0;
+            at[i] = e <= E ? __ldg(off + e) : 0;
         }
     }
 };
 
 // All threads of the block; ends with a barrier.
-__device__ void load_segments(Segments& s, const Offsets& off, int E, int64_t P, int tn_max) {
+__device__ void load_segments(const Segments& s, const Offsets& off, int E, int64_t P, int tn_max) {
 #pragma unroll
-    for (int i = 0; i < (kMaxE + kThreads - 1) / kThreads; ++i) {
+    for (int i = 0; i < Offsets::N; ++i) {
         const int e = threadIdx.x + i * kThreads;
-        if (e >= E) break;
-        const int64_t b = off.at[i][0], t = off.at[i][1];
-        const int64_t lo = b < 0 ? 0 : b > P ? P : b;
-        const int64_t hi = t > P ? P : t;
-        s.begin[e] = (int)lo;
-        s.count[e] = hi > lo ? (int)(hi - lo) : 0;
+        if (e > E) break;
+        const int64_t v = off.at[i];
+        s.begin[e] = (int)(v < 0 ? 0 : v > P ? P : v);
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        const int per = (E + 31) / 32, e0 = threadIdx.x * per;
-        unsigned long long mine = 0;
-        for (int e = e0; e < e0 + per && e < E; ++e) mine += tiles_of(s.count[e], tn_max);
-        unsigned long long incl = mine;
-#pragma unroll
+        const int per = (E + 32) / 32, e0 = threadIdx.x * per, e1 = min(e0 + per, E + 1);
+        int top = 0;
+        for (int e = e0; e < e1; ++e) top = max(top, s.begin[e]);
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            const int v = __shfl_up_sync(0xffffffffu, top, o);
+            if ((int)threadIdx.x >= o) top = max(top, v);
+        }
+        top = __shfl_up_sync(0xffffffffu, top, 1);
+        if (threadIdx.x == 0) top = 0;
+        for (int e = e0; e < e1; ++e) s.begin[e] = top = max(top, s.begin[e]);
+        __syncwarp();
+        unsigned mine = 0;
+        for (int e = e0; e < e1 && e < E; ++e) mine += tiles_of(s.count(e), tn_max);
+        unsigned incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
             if ((int)threadIdx.x >= o) incl += v;
         }
-        unsigned at = (unsigned)(incl - mine);
-        for (int e = e0; e < e0 + per && e < E; ++e) {
+        unsigned at = incl - mine;
+        for (int e = e0; e < e1 && e < E; ++e) {
             s.cum[e] = at;
-            at += tiles_of(s.count[e], tn_max);
+            at += tiles_of(s.count(e), tn_max);
         }
-        // More tiles than P rows in E segments can have: the ranges overlap,
-        // which is no permutation's doing.  No tile at all.
-        if (threadIdx.x == 31) s.cum[E] = incl > (unsigned long long)(P / tn_max + (E < P ? E : P)) ? 0u : (unsigned)incl;
+        if (threadIdx.x == 31) s.cum[E] = incl;
     }
     __syncthreads();
 }
@@ -278,17 +284,17 @@ __device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, uns
     }
     Tile t;
     t.e = lo;
-    const unsigned parts = tiles_of(s.count[lo], a.tn_max);
+    const unsigned parts = tiles_of(s.count(lo), a.tn_max);
     const unsigned in = tile - s.cum[lo] * a.tiles_f;
     const int f_pair = in / parts;
     t.f = 2 * f_pair + rank;
     const int part = in - f_pair * parts;
     // equal parts to within one unit of 32 tokens
-    const int units = (s.count[lo] + kUnit - 1) / kUnit, q = (unsigned)units / parts, more = units - q * (int)parts;
+    const int units = (s.count(lo) + kUnit - 1) / kUnit, q = (unsigned)units / parts, more = units - q * (int)parts;
     const int first = part * q + (part < more ? part : more);
     t.row0 = s.begin[lo] + first * kUnit;
     t.tn = (q + (part < more ? 1 : 0)) * kUnit;
-    const int left = s.count[lo] - first * kUnit;
+    const int left = s.count(lo) - first * kUnit;
     t.valid = left < t.tn ? left : t.tn;
     return t;
 }
@@ -682,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* epi = ring + a.stages * a.stage_bytes;
     uint8_t* sums = epi + kEpiWarps * kEpiBytes;  // split reductions: the other pairs' parts
     Control* c = reinterpret_cast<Control*>(sums + (a.split - 1) * kSumBytes);
-    Segments& seg = *reinterpret_cast<Segments*>(c + 1);
+    int* seg_at = reinterpret_cast<int*>(c + 1);
+    const Segments seg{seg_at, reinterpret_cast<unsigned*>(seg_at) + a.E + 1};
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -843,12 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- weight gradient
 constexpr int kWN = 256;                          // columns of a tile (K side), half in each CTA
-constexpr int kWStages = 5;
 constexpr int kWEpiBytes = 32 * 128;               // staged by an epilogue warp for a tile store
 constexpr int kWStageBytes = kABytes + kWN / 2 * kBK * 2;
 
-// Products of 16 tokens for the last `left` (or 64) of a segment.
+// Products of 16 tokens for the last `left` (or 64) of a segment, and whether
+// they take rows of the next segment, which have to be zeroed first.
 __device__ __forceinline__ int steps_of(int left) { return left >= kBK ? kBK / 16 : (left + 15) / 16; }
+__device__ __forceinline__ bool runs_over(int left) { return left < kBK && left % 16 != 0; }
 
 // A warp's 32 rows x 128 bytes, staged in the 128-byte swizzle of its tile
 // store: lane r holds row r, whose 16-byte piece c lies at c ^ (r % 8).
@@ -874,9 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmOut, WeightArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = ptx::smem_align<1024>(smem_raw);
-    uint8_t* epi = ring + kWStages * kWStageBytes;
+    uint8_t* epi = ring + a.stages * kWStageBytes;
     Control* c = reinterpret_cast<Control*>(epi + kEpiWarps * kWEpiBytes);
-    Segments& seg = *reinterpret_cast<Segments*>(c + 1);
+    int* seg_at = reinterpret_cast<int*>(c + 1);
+    const Segments seg{seg_at, reinterpret_cast<unsigned*>(seg_at) + a.E + 1};
     volatile int* abort_flag = &c->abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -889,19 +898,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::griddep_wait();
     Offsets offsets;
     offsets.load(a.off, a.E);
-    const uint32_t tmem = start_block(c, kWStages, 1, warp);
+    const uint32_t tmem = start_block(c, a.stages, 1, warp);
     load_segments(seg, offsets, a.E, a.P, kBK);
     const unsigned per_e = a.tiles_n * a.tiles_k, tiles = a.E * per_e;
 
     const uint32_t ring_at = ptx::smem_u32(ring);
     const uint32_t full = ptx::smem_u32(c->full), tail = ptx::smem_u32(c->tail), cut = ptx::smem_u32(c->cut),
                    empty = ptx::smem_u32(c->empty);
-    constexpr uint32_t all = kWStages * kWStageBytes;
+    const uint32_t all = a.stages * kWStageBytes;
     if (warp == 0 || warp == 2) {
         // Producers: warp 0 copies grad_out's tile, warp 2 x's.
         if (elect_one()) {
             Stages r;
-            bool ok = true;
+            bool ok = true, ready = true;  // ready: the stage at r is known to be empty
             const uint32_t full_pair = ptx::map_to_rank(full, 0);
             const CUtensorMap* tm = warp == 0 ? &tmY : &tmX;
             const uint32_t part = ring_at + (warp == 0 ? 0 : kABytes);
@@ -909,23 +918,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int e = tile / per_e;
                 const unsigned in = tile - e * per_e;
                 const int c0 = warp == 0 ? (in / a.tiles_k * 2 + rank) * kM : in % a.tiles_k * kWN + rank * (kWN / 2);
-                const int count = seg.count[e], row0 = seg.begin[e];
-                for (int p = 0; p < count; p += kBK, r.step(kWStageBytes, all)) {
-                    if (!ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
+                const int count = seg.count(e), row0 = seg.begin[e];
+                for (int p = 0; p < count; p += kBK) {
+                    if (!ready && !ptx::bar_wait<false>(empty + r.bar, r.phase ^ 1, kWaitNs)) {
                         give_up(abort_flag);
                         ok = false;
                         break;
                     }
-                    // a whole stage counts in the even CTA, for both; over one
-                    // that ends a segment this CTA's warp 3 goes first
-                    const bool whole = count - p >= kBK;
-                    const uint32_t bar = whole ? full_pair + r.bar : tail + r.bar;
+                    Stages next = r;
+                    next.step(kWStageBytes, all);
+                    ready = ptx::bar_try(empty + next.bar, next.phase ^ 1);
+                    // a stage counts in the even CTA, for both; over one that
+                    // runs into the next segment this CTA's warp 3 goes first
+                    const bool over = runs_over(count - p);
+                    const uint32_t bar = over ? tail + r.bar : full_pair + r.bar;
                     if (warp == 0) {
-                        if (!whole) ptx::bar_expect(tail + r.bar, kWStageBytes);
+                        if (over) ptx::bar_expect(tail + r.bar, kWStageBytes);
                         else if (rank == 0) ptx::bar_expect(full + r.bar, 2 * kWStageBytes);
                     }
                     ptx::tma_load(part + r.at, tm, c0, row0 + p, bar);
                     ptx::tma_load(part + r.at + 8192, tm, c0 + 64, row0 + p, bar);
+                    r = next;
                 }
             }
             if (!ok) settle();
@@ -935,12 +948,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc = ptx::idesc_bf16_m256(kWN, true, true);
             Stages r;
             Ring acc;
-            uint32_t whole_uses = 0, tail_uses = 0;  // parity of each stage's uses (bit of its barrier's offset)
-            bool ok = true;
+            // parity of each stage's uses, whole and cut (bit of its barrier's offset)
+            uint32_t uses[2] = {0, 0};
+            bool ok = true, ready = false;  // ready: the stage at r is known to be full
             const uint64_t ad0 = ptx::sdesc_sw128(ring_at, 8192, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 8192, 1024);
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
-                const int count = seg.count[tile / per_e];
+                const int count = seg.count(tile / per_e);
                 if (count == 0) continue;
                 if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
                     give_up(abort_flag);
@@ -948,17 +962,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc.s * kAccCols;
-                for (int p = 0; p < count; p += kBK, r.step(kWStageBytes, all)) {
+                for (int p = 0; p < count; p += kBK) {
                     const uint32_t bit = r.bar >> 3;
-                    const bool whole = count - p >= kBK;
-                    ok = whole ? ptx::bar_wait<true>(full + r.bar, whole_uses >> bit & 1, kWaitNs)
-                               : ptx::bar_wait<true>(cut + r.bar, tail_uses >> bit & 1, kWaitNs);
-                    if (!ok) {
-                        give_up(abort_flag);
-                        break;
+                    const bool over = runs_over(count - p);
+                    if (!ready) {
+                        ok = over ? ptx::bar_wait<true>(cut + r.bar, uses[1] >> bit & 1, kWaitNs)
+                                  : ptx::bar_wait<true>(full + r.bar, uses[0] >> bit & 1, kWaitNs);
+                        if (!ok) {
+                            give_up(abort_flag);
+                            break;
+                        }
                     }
-                    if (whole) whole_uses ^= 1u << bit;
-                    else tail_uses ^= 1u << bit;
+                    if (over) uses[1] ^= 1u << bit;
+                    else uses[0] ^= 1u << bit;
+                    Stages next = r;
+                    next.step(kWStageBytes, all);
+                    // look ahead within the segment
+                    ready = count - p > kBK && !runs_over(count - p - kBK) &&
+                            ptx::bar_try_cluster(full + next.bar, uses[0] >> (next.bar >> 3) & 1);
                     ptx::tc_fence_after();
                     const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
                     const int steps = steps_of(count - p);
@@ -967,36 +988,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kk < steps)
                             ptx::umma_bf16_pair(d, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), idesc, (p | kk) != 0);
                     ptx::umma_commit_pair(empty + r.bar, 3);
+                    r = next;
                 }
                 ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), 3);
                 acc.step(2);
             }
         }
     } else if (warp == 3) {
-        // The last stage of a segment holds rows of the next one: zero them in
-        // every box, then arrive for this CTA.
+        // A stage that runs over a segment's end: zero the next segment's rows
+        // in every box, then arrive for this CTA.
         Stages r;
-        uint32_t uses = 0;  // parity of each stage's uses as a tail
-        bool ok = true;
-        for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
-            const int count = seg.count[tile / per_e], left = count % kBK;
+        uint32_t uses = 0;  // parity of each stage's uses of its tail barrier
+        for (unsigned tile = pair; tile < tiles; tile += pairs) {
+            const int count = seg.count(tile / per_e), left = count % kBK;
             for (int p = kBK; p <= count; p += kBK) r.step(kWStageBytes, all);
             if (left == 0) continue;
-            const uint32_t bit = r.bar >> 3;
-            if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs)) {
-                if (lane == 0) give_up(abort_flag);
-                ok = false;
-                break;
+            if (runs_over(left)) {
+                const uint32_t bit = r.bar >> 3;
+                if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs)) {
+                    if (lane == 0) give_up(abort_flag);
+                    break;
+                }
+                uses ^= 1u << bit;
+                const int end = steps_of(left) * 16 * 8;  // in 16-byte pieces of a 64-column box
+#pragma unroll
+                for (int box = 0; box < kWStageBytes / 8192; ++box) {
+                    uint4* at = reinterpret_cast<uint4*>(ring + r.at + box * 8192);
+                    for (int i = left * 8 + lane; i < end; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(cut + r.bar, 0));
             }
-            uses ^= 1u << bit;
-            uint8_t* a_s = ring + r.at;
-            const int pieces = (16 * steps_of(left) - left) * 8;  // 16-byte pieces per 64-column box
-            for (int i = lane; i < pieces * (kWStageBytes / 8192); i += 32)
-                *reinterpret_cast<uint4*>(a_s + (i / pieces) * 8192 + left * 128 + (i % pieces) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(cut + r.bar, 0));
             r.step(kWStageBytes, all);
         }
     } else if (warp >= 4) {
@@ -1007,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = tile / per_e;
                 const unsigned in = tile - e * per_e;
             const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
-            const bool some = seg.count[e] > 0;
+            const bool some = seg.count(e) > 0;
             if (some) {
                 if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
                     if (lane == 0) give_up(abort_flag);
@@ -1052,27 +1075,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     end_block(tmem, warp);
 }
 
-// Column sums of the segments: a cluster of eight blocks per (expert, 256
-// columns), its 64 warps over the rows in turn, joined in warp and block order.
-// (A second pass over grad_out, 75 us of the 960 for 32768 x 7168 rows.
-// Started beside expert_weight_kernel, one block an SM, it made both last
-// 1190 us.)
+// Column sums of the segments: a cluster of up to eight blocks per (expert, 256
+// columns), its warps over the rows in turn, joined in warp and block order.
+// (A second pass over grad_out.  Started beside expert_weight_kernel, one block
+// an SM, it made both last longer: 1190 against 960 us for 32768 x 7168 rows.)
 constexpr int kBiasBlocks = 8;
 
 __global__ void __launch_bounds__(256)
-    expert_bias_kernel(const bf16* dy, const int32_t* off, int64_t P, int N, float* grad_bias) {
+    expert_bias_kernel(const bf16* dy, const int32_t* off, int64_t P, int N, int blocks, float* grad_bias) {
     __shared__ float part[8][256];
     __shared__ float joined[kBiasBlocks][256];  // the first block's is used
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank();
-    const int e = blockIdx.y, c0 = blockIdx.x / kBiasBlocks * 256, c = c0 + lane * 8;
+    const int e = blockIdx.y, c0 = blockIdx.x / blocks * 256, c = c0 + lane * 8;
     ptx::griddep_wait();
     const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
     const int64_t lo = b < 0 ? 0 : b > P ? P : b, hi = t > P ? P : t;
     float s[8] = {};
     if (c < N) {
-#pragma unroll 4
-        for (int64_t r = lo + rank * 8 + warp; r < hi; r += 8 * kBiasBlocks) {
+#pragma unroll 8
+        for (int64_t r = lo + rank * 8 + warp; r < hi; r += 8 * blocks) {
             const uint4 v = *reinterpret_cast<const uint4*>(dy + r * N + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -1094,8 +1116,7 @@ __global__ void __launch_bounds__(256)
     const int col = c0 + threadIdx.x;
     if (rank == 0 && col < N) {
         sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kBiasBlocks; ++i) sum += joined[i][threadIdx.x];
+        for (int i = 0; i < blocks; ++i) sum += joined[i][threadIdx.x];
         grad_bias[(int64_t)e * N + col] = sum;
     }
 }
@@ -1175,10 +1196,17 @@ int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t s
 int check_tiles(const char* who, int64_t tiles);
 
 constexpr size_t kSmemMax = 232448;  // 227 KB
-constexpr size_t kTail = kEpiWarps * kEpiBytes + sizeof(Control) + sizeof(Segments);
-constexpr size_t kWeightSmem = 1024 + kWStages * kWStageBytes + kEpiWarps * kWEpiBytes + sizeof(Control) + sizeof(Segments);
-static_assert(kWeightSmem <= kSmemMax, "weight gradient's shared memory");
-static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + kTail <= kSmemMax, "row products' shared memory");
+// Shared memory besides the stages: alignment, barriers, segments, staging.
+size_t fixed_bytes(int E, size_t staging) { return 1024 + sizeof(Control) + segment_bytes(E) + staging; }
+static_assert(1024 + 6 * (kABytes + 128 * kBK * 2) + sizeof(Control) + segment_bytes(kMaxE) + kEpiWarps * kEpiBytes <=
+                  kSmemMax, "row products' shared memory");
+static_assert(1024 + 5 * kWStageBytes + sizeof(Control) + segment_bytes(kMaxE) + kEpiWarps * kWEpiBytes <= kSmemMax,
+              "weight gradient's shared memory");
+
+int stages_of(size_t room, int stage_bytes) {
+    const int fit = (int)(room / stage_bytes);
+    return fit < kMaxStages ? fit : kMaxStages;
+}
 
 // Tokens per tile: enough for the experts' mean share of rows (narrow tiles
 // leave room for more stages, which a product that waits for its weights
@@ -1201,8 +1229,7 @@ void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     if (a.tn_max == 32 && most <= fit2)
         a.split = most <= fit4 && blocks_k >= 8 ? 4 : blocks_k >= 4 ? 2 : 1;
     a.stage_bytes = kABytes + a.tn_max / 2 * kBK * 2;
-    const int fit = (int)((kSmemMax - 1024 - kTail - (a.split - 1) * kSumBytes) / a.stage_bytes);
-    a.stages = fit < kMaxStages ? fit : kMaxStages;
+    a.stages = stages_of(kSmemMax - fixed_bytes(a.E, kEpiWarps * kEpiBytes + (a.split - 1) * kSumBytes), a.stage_bytes);
 }
 
 // Clusters of `split` pairs that run at once on the current device, looked up
@@ -1250,7 +1277,8 @@ int run_rows(const char* who, const CUtensorMap& tmW, const void* x, int64_t x_c
     cudaError_t err = encode_rows(&tmX, x, a.P, x_cols, 32);
     if (err == cudaSuccess) err = encode_rows(&tmX16, x, a.P, x_cols, 16);
     if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(rows)");
-    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + (a.split - 1) * kSumBytes + kTail;
+    const size_t smem = (size_t)a.stages * a.stage_bytes +
+                        fixed_bytes(a.E, kEpiWarps * kEpiBytes + (a.split - 1) * kSumBytes);
     const int blocks = a.split == 4 ? fit4 * 8 : a.split == 2 ? fit2 * 4 : sms & ~1;
     return launch(expert_rows_kernel<MODE>, dim3(blocks), 2 * a.split, kThreads, smem, who, stream, tmW, tmX, tmX16, a);
 }
@@ -1397,7 +1425,10 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     int dev = 0, sms = 0;
     int rc2 = sm_count(&dev, &sms);
     if (rc2 != MOE_OK) return rc2;
-    WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM), (unsigned)(K + kWN - 1) / kWN};
+    WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM), (unsigned)(K + kWN - 1) / kWN, 0};
+    const size_t fixed = fixed_bytes(E, kEpiWarps * kWEpiBytes);
+    a.stages = stages_of(kSmemMax - fixed, kWStageBytes);  // 6 up to 400 experts, else 5
+    const size_t smem = fixed + (size_t)a.stages * kWStageBytes;
     rc2 = check_tiles(who, (int64_t)a.E * a.tiles_n * a.tiles_k);
     if (rc2 != MOE_OK) return rc2;
     CUtensorMap tmY, tmX, tmOut;
@@ -1410,17 +1441,19 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     if (err == cudaSuccess) err = encode(&tmOut, grad_weight, 3, dims, strides, box, f32);
     if (err != cudaSuccess) return set_cuda_error(err, "cuTensorMapEncodeTiled(grad_weight)");
     if (f32) {
-        rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kWeightSmem);
+        rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kSmemMax);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, tmOut, a);
+            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut, a);
     } else {
-        rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kWeightSmem);
+        rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kSmemMax);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, kWeightSmem, who, stream, tmY, tmX, tmOut, a);
+            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut, a);
     }
     if (rc2 != MOE_OK || !grad_bias) return rc2;
-    return launch(expert_bias_kernel, dim3((N + 255) / 256 * kBiasBlocks, E), kBiasBlocks, 256, 0, who, stream,
-                  (const bf16*)grad_out, expert_offsets, P, (int)N, grad_bias);
+    int blocks = kBiasBlocks;  // with 16 rows to a warp or more
+    while (blocks > 1 && P / E < 128 * blocks) blocks /= 2;
+    return launch(expert_bias_kernel, dim3((N + 255) / 256 * blocks, E), blocks, 256, 0, who, stream,
+                  (const bf16*)grad_out, expert_offsets, P, (int)N, blocks, grad_bias);
 }
 
 }  // extern "C"
