@@ -1,7 +1,9 @@
 """The expert layer's calls against their definitions in 64 bits (GPU only):
 token sort and combine, expert products, routing gradient, and a layer of them
 forward and backward."""
-import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -255,6 +257,70 @@ def test_offsets_outside_the_rows(offsets):
     assert bool((buf[32:32 + P][rows == 0] == 3.0).all())
 
 
+@pytest.mark.parametrize("counts,K,N,gated", [
+    ([0, 1, 0, 0, 1, 0, 0, 0], 1024, 512, True),       # one token: four pairs of CTAs to a tile
+    ([3], 520, 8, False), ([32, 0, 33, 1], 4096, 136, False), ([1] * 12, 4160, 264, False),
+    ([5, 0, 31, 2], 264, 520, True), ([17], 7168, 256, False)])
+def test_few_rows_long_reductions(counts, K, N, gated):
+    """Calls small enough that pairs of CTAs share a tile's reduction: against
+    the definition, and the same bits each time."""
+    g = gen(K + N)
+    off = torch.tensor([0] + counts, device=DEV).cumsum(0).to(I32)
+    P, E = sum(counts), len(counts)
+    x, w = randn(g, P, K), randn(g, E, 2 * N if gated else N, K, scale=K ** -0.5)
+    b, r = randn(g, E, w.shape[1], dtype=F32), randn(g, P, N)
+    out = moe.expert_matmul(x, w, off, bias=b, activation="silu", gated=gated, residual=r)
+    ref.within(out, ref.matmul(x, w, off, b, "silu", gated, r)["out"])
+    for _ in range(3):
+        assert torch.equal(moe.expert_matmul(x, w, off, bias=b, activation="silu", gated=gated, residual=r), out)
+    dy, w2 = randn(g, P, K), randn(g, E, K, N, scale=K ** -0.5)
+    dx = moe.expert_matmul_grad_input(dy, w2, off)
+    ref.within(dx, ref.grad_input(dy, w2, off, None, "none", False))
+    assert torch.equal(moe.expert_matmul_grad_input(dy, w2, off), dx)
+
+
+@pytest.mark.parametrize("E", [1000, 1024])
+def test_most_experts(E):
+    g = gen(E)
+    counts = torch.randint(0, 4, (E,), generator=g, device=DEV)
+    counts[::7] = 0
+    counts[E // 2] = 300
+    off = torch.zeros(E + 1, dtype=I32, device=DEV)
+    off[1:] = counts.cumsum(0)
+    P, K, N = int(off[-1]), 72, 40
+    x, w = randn(g, P, K), randn(g, E, N, K)
+    ref.within(moe.expert_matmul(x, w, off), ref.matmul(x, w, off, None, "none", False, None)["out"])
+    dy = randn(g, P, N)
+    ref.within(moe.expert_matmul_grad_input(dy, w, off), ref.grad_input(dy, w, off, None, "none", False))
+    dw, db = moe.expert_matmul_grad_weight(dy, x, off, bias_grad=True)
+    want, want_b = ref.grad_weight(dy, x, off, E, BF)
+    ref.within(dw, want)
+    ref.within(db, want_b)
+
+
+def test_product_offsets_pass_32_bits():
+    """More than 2^31 values in the output, the preactivation and the weight's
+    gradient: their last rows against the definition."""
+    g = gen(31)
+    P, K, N = 270000, 64, 8192
+    off = torch.tensor([0, 130000, P], dtype=I32, device=DEV)
+    x, w = randn(g, P, K), randn(g, 2, N, K, scale=0.125)
+    out, kept = moe.expert_matmul(x, w, off, activation="silu", return_preact=True)
+    want = ref.matmul(x[-300:], w[1:], [0, 300], None, "silu", False, None)
+    ref.within(out[-300:], want["out"])
+    ref.within(kept[-300:], want["preact"])
+    dx = moe.expert_matmul_grad_input(out, w, off)
+    ref.within(dx[-300:], ref.grad_input(out[-300:], w[1:], [0, 300], None, "none", False))
+    del out, kept, dx, x, w
+    E, N, K = 300, 4096, 2048
+    off = torch.arange(E + 1, dtype=I32, device=DEV) * 3
+    dy, x = randn(g, 3 * E, N), randn(g, 3 * E, K)
+    dw = moe.expert_matmul_grad_weight(dy, x, off)
+    ref.within(dw[-2:], ref.grad_weight(dy[-6:], x[-6:], [0, 3, 6], 2, BF)[0])
+    del dw
+    torch.cuda.empty_cache()
+
+
 def test_expert_matmul_spread_values():
     """Preactivations far into both tails, where expf over- and underflows."""
     g = gen(13)
@@ -451,6 +517,64 @@ def test_layer_against_64_bits(M, k, E, H, F):
     for name, v in want.items():
         off = float((got[name].to(D) - v).norm() / v.norm())
         assert off <= 6 * ref.half_step(BF), (name, off)
+
+
+def test_layer_gradients_against_differences():
+    """Along random directions of each leaf, against central differences of the
+    64-bit layer: the bound of the test above on the gradient's norm times the
+    direction's, and h^2 times a third derivative."""
+    inp = layer_inputs(48, 2, 4, 72, 40, 5)
+    got = layer(*inp)
+    x, logits, W1, b1, W2, dout, k = inp
+
+    def value(*leaves):
+        a, lg, A, c, B = leaves
+        w = ref.routed(lg, got["ids"], "softmax", True, 1.0, 0.0)
+        total = a
+        for j in range(k):
+            e = got["ids"][:, j].long()
+            z = torch.einsum("mh,mnh->mn", a, A[e]) + c[e]
+            F = z.shape[1] // 2
+            total = total + w[:, j:j + 1] * torch.einsum("mf,mhf->mh", ref.f(z[:, :F], "silu") * z[:, F:], B[e])
+        return (total * dout.to(D)).sum()
+
+    leaves = [t.to(D) for t in (x, logits, W1, b1, W2)]
+    grads = [got["dx"].to(D) + dout.to(D)] + [got[n].to(D) for n in ("dlogits", "dW1", "db1", "dW2")]
+    h = 1e-4
+    for i, grad in enumerate(grads):
+        for seed in range(3):
+            d = torch.randn(grad.shape, generator=gen(seed + 7 * i), device=DEV, dtype=D)
+            up, down = list(leaves), list(leaves)
+            up[i], down[i] = leaves[i] + h * d, leaves[i] - h * d
+            want = float(value(*up) - value(*down)) / (2 * h)
+            bound = 6 * ref.half_step(BF) * float(grad.norm() * d.norm()) + 1e-5 * abs(want)
+            assert abs(float((grad * d).sum()) - want) <= bound, (i, seed)
+
+
+FIRST_CALL = """
+import torch, moe_expert_routing_token_b200 as moe
+d = "cuda:0"
+x, w = torch.ones(40, 1024, device=d).bfloat16(), torch.ones(2, 64, 1024, device=d).bfloat16()
+off = torch.tensor([0, 30, 40], dtype=torch.int32, device=d)
+out, dw = torch.zeros(40, 64, device=d).bfloat16(), torch.zeros(2, 64, 1024, device=d).bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.expert_matmul(x, w, off, out=out)
+    moe.expert_matmul_grad_weight(out, x, off, out=dw)
+assert float(out.abs().sum()) == 0
+graph.replay()
+torch.cuda.synchronize()
+assert bool((out == 1024).all()) and bool((dw[0] == 1024 * 30).all()) and bool((dw[1] == 1024 * 10).all())
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """What the library looks up once per device it may look up while a stream
+    is capturing."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_layer_captured_replayed_and_on_another_stream():
