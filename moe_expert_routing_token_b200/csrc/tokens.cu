@@ -102,9 +102,12 @@ __global__ void __launch_bounds__(kTokThreads)
 }
 
 // One warp per (token, segment): the weighted sum of the token's rows, R of
-// them in flight at a time.
+// them in flight at a time (without weights there is no residual either).
+// Narrow accesses are bound by the latency of a warp's two dependent reads,
+// places and rows: without weights, ten blocks an SM hide more of it (6 x 8191
+// fp32 rows of 1031, an eighth of the experts here: 16.1 us, 20.0 with six).
 template <typename T, int VB, bool WEIGHTED>
-__global__ void __launch_bounds__(kTokThreads)
+__global__ void __launch_bounds__(kTokThreads, VB < 16 && !WEIGHTED ? 10 : 6)
     combine_kernel(const T* y, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
                    const float* __restrict__ weights, const T* residual, T* out, int segs) {
     using C = Chunk<T, VB>;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kTokThreads)
 #pragma unroll
         for (int i = 0; i < C::N; ++i) acc[u][i] = 0.0f;
     C r[U];
-    if (residual != nullptr) {
+    if (WEIGHTED && residual != nullptr) {
         const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H);
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kTokThreads)
         C c;
 #pragma unroll
         for (int i = 0; i < C::N; ++i)
-            c.t[i] = from_f32<T>(residual != nullptr ? acc[u][i] + to_f32(r[u].t[i]) : acc[u][i]);
+            c.t[i] = from_f32<T>(WEIGHTED && residual != nullptr ? acc[u][i] + to_f32(r[u].t[i]) : acc[u][i]);
         dst[c0 + 32 * u] = c.v;
     }
 }
