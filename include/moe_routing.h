@@ -400,8 +400,9 @@ MOE_API int moe_sort_topk_by_id(float* topk_weights, int32_t* topk_ids, int64_t 
  *     once when they are stored.  Results do not depend on timing: the same
  *     inputs give the same bits.
  *   - Outputs must not overlap inputs or one another.
- *   - M * k (or P) must be below 2^31, else MOE_ERR_UNSUPPORTED.  M == 0 or
- *     P == 0 is valid (moe_expert_matmul_grad_weight then writes zeros).
+ *   - M * k must be below 2^31 and P below 2^31 - 256, else
+ *     MOE_ERR_UNSUPPORTED.  M == 0 or P == 0 is valid
+ *     (moe_expert_matmul_grad_weight then writes zeros).
  */
 
 typedef enum {
@@ -468,7 +469,8 @@ MOE_API int moe_combine_tokens_backward(const void* grad_out, const void* y, int
  *                  when gated (the gate's rows, then the other factor's)
  *   expert_offsets device, int32 (E + 1).  A plain matrix product is E = 1
  *                  with offsets {0, P}
- *   K, N           positive multiples of 8 (else MOE_ERR_UNSUPPORTED)
+ *   K, N           positive multiples of 8 up to 2^24 (else
+ *                  MOE_ERR_UNSUPPORTED)
  *   E              experts, 1 <= E <= 1024
  *   bias           device, fp32 (E, Nz), or NULL
  *   activation     f: MOE_ACT_NONE, MOE_ACT_SILU or MOE_ACT_GELU
@@ -511,6 +513,9 @@ MOE_API int moe_expert_matmul_grad_input(const void* grad_out, const void* weigh
  *   grad_weight  device, (E, N, K) of `dtype` out, 16-byte aligned
  *   grad_bias    device, fp32 (E, N) out, or NULL
  *   K, N, E      as moe_expert_matmul
+ * The products' fp32 sums are the tensor cores', which cut rather than round:
+ * an fp32 grad_weight is off by 2e-6 (2-norm, relative) for 2048 rows an
+ * expert of random signs, 5e-7 for 512.
  */
 MOE_API int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int32_t* expert_offsets,
                                           int64_t P, int32_t K, int32_t N, int32_t E, int dtype, void* grad_weight,

@@ -167,7 +167,8 @@ PyObject* gather_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t k = integer(a[2], "topk");
     rows(g, "grad_sorted");
     const int code = dtype_code(g);
-    TORCH_CHECK_VALUE(k >= 1 && g.size(0) % k == 0, "grad_sorted must have a row for each of the tokens' ", k, " slots");
+    TORCH_CHECK_VALUE(k >= 1 && g.size(0) % k == 0, "grad_sorted must have a row for each of the tokens' ", k,
+                      " slots");
     const int64_t M = g.size(0) / k, H = g.size(1);
     places(scatter, M * k, g);
     on_gpu(g, "grad_sorted");
@@ -322,8 +323,8 @@ PyObject* expert_matmul_grad_weight(PyObject*, PyObject* const* a, Py_ssize_t n)
     Tensor out = output(a[5], "out", {E, N, K}, dtype, g), db;
     if (bias) db = output(Py_None, "grad_bias", {E, N}, kF32, g);
     Launch l(g);
-    check(moe_expert_matmul_grad_weight(g.const_data_ptr(), x.const_data_ptr(), (const int32_t*)offsets.const_data_ptr(),
-                                        P, i32(K, "K"), i32(N, "N"), i32(E, "E"), dtype_code(out),
+    check(moe_expert_matmul_grad_weight(g.const_data_ptr(), x.const_data_ptr(),
+                                        (const int32_t*)offsets.const_data_ptr(), P, i32(K, "K"), i32(N, "N"), i32(E, "E"), dtype_code(out),
                                         out.mutable_data_ptr(), bias ? (float*)db.mutable_data_ptr() : nullptr,
                                         l.stream),
           "moe_expert_matmul_grad_weight");

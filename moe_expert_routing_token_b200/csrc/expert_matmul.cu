@@ -5,28 +5,39 @@
 //   moe_expert_matmul_grad_input   grad_x[p] = (W_e^T grad_out[p]) through f' at preact[p]
 //   moe_expert_matmul_grad_weight  grad_W_e = sum_p grad_out[p] x[p]^T, grad_b_e = sum_p grad_out[p]
 //
-// Two persistent kernels, one CTA per SM, warp-specialised: a TMA producer, an
-// MMA issuer and eight epilogue warps around a ring of shared-memory stages
-// and two TMEM accumulators, so that a tile's epilogue overlaps the next
-// tile's products.
+// Two persistent kernels on CTA pairs, one CTA per SM, warp-specialised: two
+// copying lanes, an issuing lane in the even CTA and eight epilogue warps
+// around a ring of shared-memory stages and two TMEM accumulators, so that a
+// tile's epilogue overlaps the next tile's products.  tcgen05.mma works on the
+// pair (cta_group::2, M = 256): each CTA copies its own half of both operands
+// and holds its own 128 rows of the result.
 //
-// expert_rows_kernel (the first two calls).  A tile is 128 rows of the WEIGHT
-// times up to 256 tokens of one expert: the accumulator's 128 lanes are output
+// expert_rows_kernel (the first two calls).  A tile is 256 rows of the WEIGHT
+// times up to 256 tokens of one expert: the accumulator's lanes are output
 // features and its columns tokens.  Segments have any length, and the column
-// count of tcgen05.mma goes in steps of 16, so a segment is cut into equal
-// parts of at most 256 tokens, rounded up to 16, instead of being padded to
-// 128 rows; and a handful of tokens costs one narrow product over weights that
+// count of a pair's product goes in steps of 32, so a segment is cut into equal
+// parts of at most 256 tokens in units of 32 instead of being padded to 128 or
+// 256 rows; and a handful of tokens costs one narrow product over weights that
 // stream past once.  grad_input differs only in the weight's orientation (its
-// tile is MN-major: reduction along the weight's rows).  A gated tile holds 64
-// gate and 64 up rows interleaved by 8, so that both factors of an output meet
-// in one thread's TMEM fragment.  The epilogue reads 16x256b fragments, works
-// in fp32, and turns them token-major with transposing matrix moves through
+// tile is MN-major: reduction along the weight's rows).  A gated tile holds
+// gate and up rows interleaved by 8, so that both factors of an output meet in
+// one thread's TMEM fragment.  The epilogue reads 16x256b fragments, works in
+// fp32, and turns them token-major with transposing matrix moves through
 // 80-byte shared-memory rows (a pitch without bank conflicts).
 //
-// expert_weight_kernel (grad_weight).  A tile is 128 x 256 of one expert's
-// gradient, both operands MN-major with the reduction along tokens.  The rows
-// behind a segment's end, which the last 64-row stage also brings, are zeroed
-// in shared memory before the product.
+// expert_weight_kernel (grad_weight).  A tile is 256 x 256 of one expert's
+// gradient, both operands MN-major with the reduction along tokens.  Where a
+// segment's last 64-row stage runs over its end, the next segment's rows are
+// zeroed in shared memory before the product.  The result leaves by tile
+// stores, which clip at the matrix's ends.
+//
+// What bounds them (B200): long reductions over many rows, a pair's two SMs
+// taking 64 bytes a cycle each from L2 (256 x 256 x 64 takes 516 cycles and
+// brings 32 KB to either), 83% of the tensor pipe at 8 experts of 1024 rows,
+// 7168 by 2 x 2048; under a lasting load the board's 1000 W, which lowers the
+// clock to 1.05 - 1.3 GHz (1.70 ms for 32 such experts, 1130 TFLOP/s).  Few
+// rows per expert: the weights' bytes from HBM (6.9 TB/s at 2 rows each).  Few
+// tiles: one tile's latency.
 //
 // Every wait is bounded; a wait that runs out is counted
 // (moe_watchdog_trips) and ends the block's work.
@@ -65,6 +76,7 @@ constexpr int kPitch = 80;              // bytes of a staged token: 32 features 
 constexpr int kEpiBytes = 32 * kPitch;  // per epilogue warp: 32 tokens
 constexpr int kSumBytes = kM * 32 * 4;  // a CTA's fp32 sums of a 32-token tile
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kStageNs = 2000;     // and per stage of a reduction that is waited for as a whole
 
 static __device__ unsigned int g_watchdog_trips_experts;
 
@@ -290,7 +302,7 @@ __device__ __forceinline__ Tile tile_at(const Segments& s, const RowArgs& a, uns
     t.f = 2 * f_pair + rank;
     const int part = in - f_pair * parts;
     // equal parts to within one unit of 32 tokens
-    const int units = (s.count(lo) + kUnit - 1) / kUnit, q = (unsigned)units / parts, more = units - q * (int)parts;
+    const int units = tiles_of(s.count(lo), kUnit), q = (unsigned)units / parts, more = units - q * (int)parts;
     const int first = part * q + (part < more ? part : more);
     t.row0 = s.begin[lo] + first * kUnit;
     t.tn = (q + (part < more ? 1 : 0)) * kUnit;
@@ -463,7 +475,8 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, const uint8_t* sums, in
     float acc[2][4][4];
     ptx::tmem_ld_frag32(taddr, acc);
     for (int part = 0; part < parts; ++part) {
-        const float4* from = reinterpret_cast<const float4*>(sums + part * kSumBytes + quarter * (kSumBytes / 4)) + lane;
+        const float4* from =
+            reinterpret_cast<const float4*>(sums + part * kSumBytes + quarter * (kSumBytes / 4)) + lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 v = from[i * 32];
@@ -770,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring acc;
             bool ok = true, ready = false;  // ready: the stage at r is known to be full
             // descriptors of the first stage's operands; steps of 16 in the reduction
-            const uint64_t ad0 = GRAD ? ptx::sdesc_sw128(ring_at, kABytes / 2, 1024) : ptx::sdesc_sw128(ring_at, 16, 1024);
+            const uint64_t ad0 = ptx::sdesc_sw128(ring_at, GRAD ? kABytes / 2 : 16, 1024);
             const uint64_t bd0 = ptx::sdesc_sw128(ring_at + kABytes, 16, 1024);
             const uint16_t ctas = (uint16_t)(3u << lead);
             constexpr uint64_t A_STEP = GRAD ? 2048 >> 4 : 32 >> 4, B_STEP = 32 >> 4;
@@ -814,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Bias<MODE> bias;
             bias.load(a, t, quarter, lane);
             prefetch_extra<MODE>(a, t, quarter, half, lane);
-            if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
+            if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs + blocks_k * kStageNs)) {
                 if (lane == 0) give_up(abort_flag);
                 *abort_flag = 1;
             }
@@ -827,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (slice > 0) {
                     send_sums(base, ptx::smem_u32(sums) + (slice - 1) * kSumBytes, ptx::smem_u32(&c->joined), rank,
                               quarter, lane);
-                } else if (ptx::mbar_wait_cluster(&c->joined, 0, kWaitNs)) {
+                } else if (ptx::mbar_wait_cluster(&c->joined, 0, kWaitNs + blocks_k * kStageNs)) {
                     __syncwarp();
                     add_sums(base, sums, a.split - 1, quarter, lane);
                 } else {
@@ -1029,10 +1042,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (unsigned tile = pair; tile < tiles; tile += pairs) {
             const int e = tile / per_e;
                 const unsigned in = tile - e * per_e;
-            const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32, k0 = in % a.tiles_k * kWN + half * (kWN / 2);
+            const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32;
+            const int k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count(e) > 0;
             if (some) {
-                if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs)) {
+                if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs + seg.count(e) / kBK * kStageNs)) {
                     if (lane == 0) give_up(abort_flag);
                     *abort_flag = 1;
                 }
@@ -1148,8 +1162,9 @@ cudaError_t encode(CUtensorMap* map, const void* base, int rank, const uint64_t*
         one[i] = 1;
         if (i > 0) st[i - 1] = strides[i - 1] * (f32 ? 4 : 2);
     }
-    CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                    const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -1174,7 +1189,8 @@ int allow_smem(const void* kern, int dev, size_t bytes) {
 }
 
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t smem, const char* who, void* stream, Args... args) {
+int launch(void (*kern)(KArgs...), dim3 grid, int cluster, int threads, size_t smem, const char* who, void* stream,
+           Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
@@ -1212,7 +1228,7 @@ int stages_of(size_t room, int stage_bytes) {
 // leave room for more stages, which a product that waits for its weights
 // needs), but no more than lets the tiles reach every pair of SMs: a call of
 // few tiles takes as long as one of them.  (2-slot batch of 3373 tokens, one
-// expert here, 200 x 232 with every part of the epilogue: 9.9 us with tiles of
+// expert here, 200 x 232 with every part of the epilogue: 9.4 us with tiles of
 // 32, 15.2 with tiles of 256.)
 void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
@@ -1221,7 +1237,7 @@ void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     // Where even tiles of 32 leave most SMs idle, 2 or 4 pairs share a tile's
     // reduction: a tile's time is then its weight's rows through one pair's
     // L2 ports (46 bytes a cycle and SM).  One token, 2 of 8 experts, 1024 by
-    // 2 x 512: 7.4 us with four pairs, 8.1 with one; 16 rows of 20 experts,
+    // 2 x 512: 7.5 us with four pairs, 8.1 with one; 16 rows of 20 experts,
     // 1888 by 248: 10.7 and 12.9.  Only where all clusters run at once, so that
     // each has at most one tile, whose sums need no second buffer.
     a.split = 1;
@@ -1303,8 +1319,9 @@ int check_sizes(const char* who, int64_t P, int K, int N, int E, int activation,
         snprintf(msg, sizeof msg, "%s: K=%d and N=%d must be multiples of 8", who, K, N);
         return set_error(MOE_ERR_UNSUPPORTED, msg);
     }
-    if (E > 1024 || P >= (1ll << 31) || K > (1 << 24) || N > (1 << 24)) {
-        snprintf(msg, sizeof msg, "%s: E=%d > 1024, P=%lld >= 2^31, or K=%d or N=%d > 2^24", who, E, (long long)P, K, N);
+    if (E > kMaxE || P >= (1ll << 31) - 256 || K > (1 << 24) || N > (1 << 24)) {
+        snprintf(msg, sizeof msg, "%s: E=%d > 1024, P=%lld >= 2^31 - 256, or K=%d or N=%d > 2^24", who, E,
+                 (long long)P, K, N);
         return set_error(MOE_ERR_UNSUPPORTED, msg);
     }
     return MOE_OK;
@@ -1425,7 +1442,8 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     int dev = 0, sms = 0;
     int rc2 = sm_count(&dev, &sms);
     if (rc2 != MOE_OK) return rc2;
-    WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM), (unsigned)(K + kWN - 1) / kWN, 0};
+    WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM),
+                    (unsigned)(K + kWN - 1) / kWN, 0};
     const size_t fixed = fixed_bytes(E, kEpiWarps * kWEpiBytes);
     a.stages = stages_of(kSmemMax - fixed, kWStageBytes);  // 6 up to 400 experts, else 5
     const size_t smem = fixed + (size_t)a.stages * kWStageBytes;
@@ -1443,11 +1461,13 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     if (f32) {
         rc2 = allow_smem((const void*)expert_weight_kernel<float>, dev, kSmemMax);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut, a);
+            rc2 = launch(expert_weight_kernel<float>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut,
+                         a);
     } else {
         rc2 = allow_smem((const void*)expert_weight_kernel<bf16>, dev, kSmemMax);
         if (rc2 == MOE_OK)
-            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut, a);
+            rc2 = launch(expert_weight_kernel<bf16>, dim3(sms & ~1), 2, kThreads, smem, who, stream, tmY, tmX, tmOut,
+                         a);
     }
     if (rc2 != MOE_OK || !grad_bias) return rc2;
     int blocks = kBiasBlocks;  // with 16 rows to a warp or more

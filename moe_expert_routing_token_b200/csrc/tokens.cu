@@ -270,7 +270,8 @@ struct TokArgs {
 };
 
 // Shared checks.  Returns MOE_OK to go on, -1 for an empty batch.
-int check(const TokArgs& a, int dtype, std::initializer_list<const void*> rows, std::initializer_list<const void*> words) {
+int check(const TokArgs& a, int dtype, std::initializer_list<const void*> rows,
+          std::initializer_list<const void*> words) {
     char msg[256];
     if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) {
         snprintf(msg, sizeof msg, "%s: dtype %d is neither MOE_DTYPE_F32 nor MOE_DTYPE_BF16", a.who, dtype);

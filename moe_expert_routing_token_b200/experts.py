@@ -24,7 +24,8 @@ give, and calls the C entry point on the operands' device and current stream
 (csrc/binding.cpp: through ctypes, a decode-sized call would spend three times
 its kernel's time on that).  Rows behind the last expert's segment are not
 written: freshly allocated outputs hold anything there.  Outputs must not
-overlap inputs.  A tensor that was made on another stream is the caller's to
+overlap inputs.  The functions record nothing for autograd: the backward calls
+are made by name, as above.  A tensor that was made on another stream is the caller's to
 order and, where it is freed early, to ``record_stream``.
 """
 from __future__ import annotations

@@ -132,7 +132,7 @@ I32, I64, F16, F32 = torch.int32, torch.int64, torch.float16, torch.float32
     (lambda: moe.gather_tokens(t(4, 8), t(7, dtype=I32), 2), "scatter_indx"),
     (lambda: moe.gather_tokens(t(4, 8), t(0, dtype=I32), 0), "positive"),
     (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I64), 2), "scatter_indx"),
-    (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32, ), 1 << 40), "out of range"),
+    (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32), 1 << 40), "out of range"),
     (lambda: moe.gather_tokens(t(4, 8), t(8, dtype=I32), 2), "x must be a CUDA tensor"),
     (lambda: moe.gather_tokens_backward(t(7, 8), t(7, dtype=I32), 2), "grad_sorted"),
     (lambda: moe.gather_tokens_backward(t(8, 8), t(8, dtype=I32), 2), "CUDA"),
@@ -142,7 +142,8 @@ I32, I64, F16, F32 = torch.int32, torch.int64, torch.float16, torch.float32
     (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32), residual=t(4, 8, dtype=F32)), "residual"),
     (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32), residual=t(8, 8)), "residual"),
     (lambda: moe.combine_tokens(t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "CUDA"),
-    (lambda: moe.combine_tokens_backward(t(4, 8), t(8, 8, dtype=F32), t(8, dtype=I32), t(4, 2, dtype=F32)), "y must be"),
+    (lambda: moe.combine_tokens_backward(t(4, 8), t(8, 8, dtype=F32), t(8, dtype=I32), t(4, 2, dtype=F32)),
+     "y must be"),
     (lambda: moe.combine_tokens_backward(t(5, 8), t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "grad_out must have"),
     (lambda: moe.combine_tokens_backward(t(4, 8), t(8, 8), t(8, dtype=I32), t(4, 2, dtype=F32)), "CUDA"),
     (lambda: moe.expert_matmul(t(4, 8, dtype=F32), t(2, 8, 8), t(3, dtype=I32)), "x must be bfloat16"),

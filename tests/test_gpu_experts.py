@@ -416,7 +416,8 @@ def test_topk_backward_against_differences(scoring, renorm, rsf, cap):
 def test_topk_backward_saturated_logits():
     for scoring, renorm, rsf, cap in ROUTES:
         x, ids, dw = choice(40, 8, 256, F32, 9, scale=30.0)
-        check_topk(x, ids, dw, scoring, renorm, rsf, cap, moe.topk_backward(dw, x, ids, scoring, renorm, rsf, softcap=cap))
+        got = moe.topk_backward(dw, x, ids, scoring, renorm, rsf, softcap=cap)
+        check_topk(x, ids, dw, scoring, renorm, rsf, cap, got)
 
 
 def test_topk_backward_ids_outside_and_twice():
