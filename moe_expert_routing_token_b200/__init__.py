@@ -1,4 +1,5 @@
-"""B200-native (sm_100a) Mixture-of-Experts token-to-expert routing.
+"""B200-native (sm_100a) Mixture-of-Experts token-to-expert routing, and the
+expert layer that it feeds.
 
 The compute lives in ``libmoe_routing.so`` (hand-written CUDA kernels behind
 the C ABI in ``include/moe_routing.h``); this package is its thin binding.
