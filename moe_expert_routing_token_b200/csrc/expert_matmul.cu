@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t part = ring_at + (warp == 0 ? 0 : kABytes);
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
                 const int e = tile / per_e;
-                const unsigned in = tile - e * per_e;
+            const unsigned in = tile - e * per_e;
                 const int c0 = warp == 0 ? (in / a.tiles_k * 2 + rank) * kM : in % a.tiles_k * kWN + rank * (kWN / 2);
                 const int count = seg.count(e), row0 = seg.begin[e];
                 for (int p = 0; p < count; p += kBK) {
@@ -1016,17 +1016,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A stage that runs over a segment's end: zero the next segment's rows
         // in every box, then arrive for this CTA.
         Stages r;
-        uint32_t uses = 0;  // parity of each stage's uses of its tail barrier
+        uint32_t uses = 0;    // parity of each stage's uses of its tail barrier
+        uint64_t before = 0;  // stages up to the next wait, which lasts as long as they take
         for (unsigned tile = pair; tile < tiles; tile += pairs) {
             const int count = seg.count(tile / per_e), left = count % kBK;
-            for (int p = kBK; p <= count; p += kBK) r.step(kWStageBytes, all);
+            before += (count + kBK - 1) / kBK;
+            for (int p = count / kBK; p > 0; --p) r.step(kWStageBytes, all);
             if (left == 0) continue;
             if (runs_over(left)) {
                 const uint32_t bit = r.bar >> 3;
-                if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs)) {
+                if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs + before * kStageNs)) {
                     if (lane == 0) give_up(abort_flag);
                     break;
                 }
+                before = 0;
                 uses ^= 1u << bit;
                 const int end = steps_of(left) * 16 * 8;  // in 16-byte pieces of a 64-column box
 #pragma unroll
@@ -1046,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring acc;
         for (unsigned tile = pair; tile < tiles; tile += pairs) {
             const int e = tile / per_e;
-                const unsigned in = tile - e * per_e;
+            const unsigned in = tile - e * per_e;
             const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32;
             const int k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count(e) > 0;
