@@ -1110,6 +1110,7 @@ __global__ void __launch_bounds__(256)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank();
     const int e = blockIdx.y, c0 = blockIdx.x / blocks * 256, c = c0 + lane * 8;
+    ptx::cluster_arrive();  // waited for before the first access to another block's shared memory
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int64_t b = __ldg(off + e), t = __ldg(off + e + 1);
@@ -1134,6 +1135,7 @@ __global__ void __launch_bounds__(256)
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) sum += part[w][threadIdx.x];
+    ptx::cluster_wait();
     ptx::st_cluster_u32(ptx::map_to_rank(ptx::smem_u32(&joined[rank][threadIdx.x]), 0), __float_as_uint(sum));
     ptx::cluster_sync();
     const int col = c0 + threadIdx.x;

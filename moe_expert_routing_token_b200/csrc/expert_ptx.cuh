@@ -181,6 +181,11 @@ __device__ __forceinline__ void bar_arrive_remote(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// The two halves of a cluster barrier that orders no memory: after the wait,
+// every block of the cluster has started.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // ---------------------------------------------------------------- pairs of floats
 // Two fp32 operations per instruction.
 __device__ __forceinline__ unsigned long long pair_of(float2 v) {
