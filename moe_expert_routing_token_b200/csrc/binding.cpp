@@ -71,12 +71,14 @@ void expect(const Tensor& t, const char* name, at::IntArrayRef shape, at::Scalar
                       name, " must be a contiguous ", shape_text(shape), " ", dtype, " tensor on ", beside.device());
 }
 
-// The given tensor, checked, or a new one on the device of `beside`.
-Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType dtype, const Tensor& beside) {
-    if (o != Py_None) {
-        const Tensor& t = tensor(o, name);
-        expect(t, name, shape, dtype, beside);
-        return t;
+// The tensor given for an output, or none.
+const Tensor* given(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
+
+// That tensor, checked, or a new one on the device of `beside`.
+Tensor output(const Tensor* t, const char* name, at::IntArrayRef shape, at::ScalarType dtype, const Tensor& beside) {
+    if (t != nullptr) {
+        expect(*t, name, shape, dtype, beside);
+        return *t;
     }
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(beside.device()));
 }
@@ -97,18 +99,29 @@ void on_gpu(const Tensor& t, const char* name) {
     TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor");
 }
 
-// Makes the operands' device current while it lives, and knows its stream.
+// Around allocations and launches: makes the operands' device current, knows
+// its stream, and lets other Python threads run, as either may wait for the
+// device.
 struct Launch {
     c10::cuda::OptionalCUDAGuard guard;
     void* stream;
+    PyThreadState* state;
     explicit Launch(const Tensor& t) {
         const auto index = t.device().index();
         if (c10::cuda::current_device() != index) guard.set_index(index);
         stream = c10::cuda::getCurrentCUDAStream(index).stream();
+        state = PyEval_SaveThread();
+    }
+    Launch(const Launch&) = delete;
+    ~Launch() { lock(); }
+    void lock() {
+        if (state != nullptr) PyEval_RestoreThread(state);
+        state = nullptr;
     }
 };
 
-void check(int status, const char* name) {
+void check(Launch& l, int status, const char* name) {
+    l.lock();
     if (status == MOE_OK) return;
     const std::string text = std::string(name) + ": " + moe_last_error();
     PyObject* kind = status == MOE_ERR_INVALID_ARG ? PyExc_ValueError
@@ -150,10 +163,11 @@ PyObject* gather_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = x.size(0), H = x.size(1);
     places(scatter, M * k, x);
     on_gpu(x, "x");
-    Tensor out = output(a[3], "out", {M * k, H}, x.scalar_type(), x);
+    const Tensor* to = given(a[3], "out");
     Launch l(x);
-    check(moe_gather_tokens(x.const_data_ptr(), code, M, i32(H, "H"), (const int32_t*)scatter.const_data_ptr(), (int)k,
-                            out.mutable_data_ptr(), l.stream),
+    Tensor out = output(to, "out", {M * k, H}, x.scalar_type(), x);
+    check(l, moe_gather_tokens(x.const_data_ptr(), code, M, i32(H, "H"), (const int32_t*)scatter.const_data_ptr(),
+                               (int)k, out.mutable_data_ptr(), l.stream),
           "moe_gather_tokens");
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -172,11 +186,12 @@ PyObject* gather_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t M = g.size(0) / k, H = g.size(1);
     places(scatter, M * k, g);
     on_gpu(g, "grad_sorted");
-    Tensor out = output(a[3], "out", {M, H}, g.scalar_type(), g);
+    const Tensor* to = given(a[3], "out");
     Launch l(g);
-    check(moe_gather_tokens_backward(g.const_data_ptr(), code, M, i32(H, "H"),
-                                     (const int32_t*)scatter.const_data_ptr(), (int)k, out.mutable_data_ptr(),
-                                     l.stream),
+    Tensor out = output(to, "out", {M, H}, g.scalar_type(), g);
+    check(l, moe_gather_tokens_backward(g.const_data_ptr(), code, M, i32(H, "H"),
+                                        (const int32_t*)scatter.const_data_ptr(), (int)k, out.mutable_data_ptr(),
+                                        l.stream),
           "moe_gather_tokens_backward");
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -197,11 +212,12 @@ PyObject* combine_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& r = a[3] == Py_None ? y : tensor(a[3], "residual");
     if (a[3] != Py_None) expect(r, "residual", {M, H}, y.scalar_type(), y);
     on_gpu(y, "y");
-    Tensor out = output(a[4], "out", {M, H}, y.scalar_type(), y);
+    const Tensor* to = given(a[4], "out");
     Launch l(y);
-    check(moe_combine_tokens(y.const_data_ptr(), code, M, i32(H, "H"), (const int32_t*)scatter.const_data_ptr(),
-                             i32(k, "topk"), (const float*)w.const_data_ptr(), data(a[3], r), out.mutable_data_ptr(),
-                             l.stream),
+    Tensor out = output(to, "out", {M, H}, y.scalar_type(), y);
+    check(l, moe_combine_tokens(y.const_data_ptr(), code, M, i32(H, "H"), (const int32_t*)scatter.const_data_ptr(),
+                                i32(k, "topk"), (const float*)w.const_data_ptr(), data(a[3], r),
+                                out.mutable_data_ptr(), l.stream),
           "moe_combine_tokens");
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -222,13 +238,14 @@ PyObject* combine_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(y, "y", {M * k, H}, g.scalar_type(), g);
     places(scatter, M * k, g);
     on_gpu(g, "grad_out");
-    Tensor gy = output(a[4], "grad_y", {M * k, H}, g.scalar_type(), g);
-    Tensor gw = output(a[5], "grad_weights", {M, k}, kF32, g);
+    const Tensor *to_y = given(a[4], "grad_y"), *to_w = given(a[5], "grad_weights");
     Launch l(g);
-    check(moe_combine_tokens_backward(g.const_data_ptr(), y.const_data_ptr(), code, M, i32(H, "H"),
-                                      (const int32_t*)scatter.const_data_ptr(), i32(k, "topk"),
-                                      (const float*)w.const_data_ptr(), gy.mutable_data_ptr(),
-                                      (float*)gw.mutable_data_ptr(), l.stream),
+    Tensor gy = output(to_y, "grad_y", {M * k, H}, g.scalar_type(), g);
+    Tensor gw = output(to_w, "grad_weights", {M, k}, kF32, g);
+    check(l, moe_combine_tokens_backward(g.const_data_ptr(), y.const_data_ptr(), code, M, i32(H, "H"),
+                                         (const int32_t*)scatter.const_data_ptr(), i32(k, "topk"),
+                                         (const float*)w.const_data_ptr(), gy.mutable_data_ptr(),
+                                         (float*)gw.mutable_data_ptr(), l.stream),
           "moe_combine_tokens_backward");
     return two(gy, gw);
     END_HANDLE_TH_ERRORS
@@ -268,13 +285,14 @@ PyObject* expert_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[3] != Py_None) expect(bias, "bias", {E, Nz}, kF32, x);
     if (a[6] != Py_None) expect(residual, "residual", {P, N}, kBf16, x);
     on_gpu(x, "x");
-    Tensor out = output(a[8], "out", {P, N}, kBf16, x), preact;
-    if (kept) preact = output(a[9], "preact_out", {P, Nz}, kBf16, x);
+    const Tensor *to = given(a[8], "out"), *to_preact = given(a[9], "preact_out");
     Launch l(x);
-    check(moe_expert_matmul(x.const_data_ptr(), w.const_data_ptr(), (const int32_t*)offsets.const_data_ptr(), P,
-                            i32(K, "K"), i32(N, "N"), i32(E, "E"), (const float*)data(a[3], bias), (int)act, gated,
-                            data(a[6], residual), out.mutable_data_ptr(), kept ? preact.mutable_data_ptr() : nullptr,
-                            l.stream),
+    Tensor out = output(to, "out", {P, N}, kBf16, x), preact;
+    if (kept) preact = output(to_preact, "preact_out", {P, Nz}, kBf16, x);
+    check(l, moe_expert_matmul(x.const_data_ptr(), w.const_data_ptr(), (const int32_t*)offsets.const_data_ptr(), P,
+                               i32(K, "K"), i32(N, "N"), i32(E, "E"), (const float*)data(a[3], bias), (int)act,
+                               gated, data(a[6], residual), out.mutable_data_ptr(),
+                               kept ? preact.mutable_data_ptr() : nullptr, l.stream),
           "moe_expert_matmul");
     return kept ? two(out, preact) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -296,11 +314,13 @@ PyObject* expert_matmul_grad_input(PyObject*, PyObject* const* a, Py_ssize_t n) 
     const Tensor& preact = a[3] == Py_None ? g : tensor(a[3], "preact");
     if (a[3] != Py_None) expect(preact, "preact", {P, width}, kBf16, g);
     on_gpu(g, "grad_out");
-    Tensor out = output(a[6], "out", {P, width}, kBf16, g);
+    const Tensor* to = given(a[6], "out");
     Launch l(g);
-    check(moe_expert_matmul_grad_input(g.const_data_ptr(), w.const_data_ptr(), (const int32_t*)offsets.const_data_ptr(),
-                                       P, i32(K, "K"), i32(N, "N"), i32(E, "E"), data(a[3], preact), (int)act, gated,
-                                       out.mutable_data_ptr(), l.stream),
+    Tensor out = output(to, "out", {P, width}, kBf16, g);
+    check(l, moe_expert_matmul_grad_input(g.const_data_ptr(), w.const_data_ptr(),
+                                          (const int32_t*)offsets.const_data_ptr(), P, i32(K, "K"), i32(N, "N"),
+                                          i32(E, "E"), data(a[3], preact), (int)act, gated, out.mutable_data_ptr(),
+                                          l.stream),
           "moe_expert_matmul_grad_input");
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -317,16 +337,17 @@ PyObject* expert_matmul_grad_weight(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t P = g.size(0), N = g.size(1), K = x.size(1);
     expect(x, "x", {P, K}, kBf16, g);
     auto dtype = truth(a[4]) ? kF32 : kBf16;
-    if (a[5] != Py_None) dtype = tensor(a[5], "out").scalar_type();
+    const Tensor* to = given(a[5], "out");
+    if (to != nullptr) dtype = to->scalar_type();
     TORCH_CHECK_VALUE(dtype == kF32 || dtype == kBf16, "unsupported dtype ", dtype, "; expected float32 or bfloat16");
     on_gpu(g, "grad_out");
-    Tensor out = output(a[5], "out", {E, N, K}, dtype, g), db;
-    if (bias) db = output(Py_None, "grad_bias", {E, N}, kF32, g);
     Launch l(g);
-    check(moe_expert_matmul_grad_weight(g.const_data_ptr(), x.const_data_ptr(),
-                                        (const int32_t*)offsets.const_data_ptr(), P, i32(K, "K"), i32(N, "N"), i32(E, "E"), dtype_code(out),
-                                        out.mutable_data_ptr(), bias ? (float*)db.mutable_data_ptr() : nullptr,
-                                        l.stream),
+    Tensor out = output(to, "out", {E, N, K}, dtype, g), db;
+    if (bias) db = output(nullptr, "grad_bias", {E, N}, kF32, g);
+    check(l, moe_expert_matmul_grad_weight(g.const_data_ptr(), x.const_data_ptr(),
+                                           (const int32_t*)offsets.const_data_ptr(), P, i32(K, "K"), i32(N, "N"),
+                                           i32(E, "E"), dtype_code(out), out.mutable_data_ptr(),
+                                           bias ? (float*)db.mutable_data_ptr() : nullptr, l.stream),
           "moe_expert_matmul_grad_weight");
     return bias ? two(out, db) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
@@ -347,11 +368,12 @@ PyObject* topk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(ids, "topk_ids", {M, k}, kI32, x);
     expect(g, "grad_weights", {M, k}, kF32, x);
     on_gpu(x, "gating_output");
-    Tensor out = output(a[7], "out", {M, E}, x.scalar_type(), x);
+    const Tensor* to = given(a[7], "out");
     Launch l(x);
-    check(moe_topk_backward((const float*)g.const_data_ptr(), x.const_data_ptr(), code,
-                            (const int32_t*)ids.const_data_ptr(), M, i32(E, "E"), i32(k, "topk"), (int)scoring, renorm,
-                            (float)rsf, (float)cap, out.mutable_data_ptr(), l.stream),
+    Tensor out = output(to, "out", {M, E}, x.scalar_type(), x);
+    check(l, moe_topk_backward((const float*)g.const_data_ptr(), x.const_data_ptr(), code,
+                               (const int32_t*)ids.const_data_ptr(), M, i32(E, "E"), i32(k, "topk"), (int)scoring,
+                               renorm, (float)rsf, (float)cap, out.mutable_data_ptr(), l.stream),
           "moe_topk_backward");
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS

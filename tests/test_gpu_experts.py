@@ -4,6 +4,7 @@ forward and backward."""
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -604,6 +605,26 @@ def test_layer_captured_replayed_and_on_another_stream():
             for name in held:
                 assert torch.equal(held[name], alone[k][name]), name
                 assert torch.equal(beside[name], alone[k][name]), name
+
+
+def test_layers_of_two_threads():
+    """Two threads call the layer at once, each on a stream of its own: the
+    same bits as one after the other."""
+    inputs = [layer_inputs(97, 4, 16, 200, 136, 3), layer_inputs(3, 2, 16, 264, 40, 4)]
+    alone = [layer(*i) for i in inputs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            done = [layer(*inputs[i]) for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+        return done
+
+    with ThreadPoolExecutor(2) as pool:
+        for i, done in enumerate(pool.map(run, range(2))):
+            for got in done:
+                for name in got:
+                    assert torch.equal(got[name], alone[i][name]), (i, name)
 
 
 def test_no_watchdog_trips():
