@@ -62,63 +62,80 @@ __device__ __forceinline__ uint32_t places(const int32_t* scatter, int64_t t, in
     return __ballot_sync(0xffffffffu, *place < P);
 }
 
-// Accesses a lane has in flight per row: 64 bytes, at most 16 accesses.
-template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : VB >= 8 ? 8 : 16; }
+// Accesses a lane has in flight per row: 64 bytes, at most 12 accesses; for sums
+// half of that, at most 9.
+template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : VB >= 8 ? 8 : 12; }
+template <int VB> constexpr int sum_unroll() { return VB >= 16 ? 2 : VB >= 8 ? 4 : 9; }
 
-// One warp per (token, segment of 32 * U accesses of the row).
+// A row's n accesses in `segs` even segments of up to 32 * U (a multiple of 32):
+// a short last one costs as much latency as a whole one.  The warps of a block
+// have the same segment of consecutive tokens.
+struct Split {
+    uint32_t segs, span;
+    Split(int64_t n, int U) {
+        segs = (uint32_t)((n + 32 * U - 1) / (32 * U));
+        span = (uint32_t)((n + 32 * (int64_t)segs - 1) / (32 * (int64_t)segs)) * 32;
+    }
+};
+
+// One warp per (token, segment).
 template <typename T, int VB>
 __global__ void __launch_bounds__(kTokThreads)
     gather_kernel(const T* x, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
-                  T* sorted, int segs) {
+                  T* sorted, uint32_t segs, uint32_t span) {
     using C = Chunk<T, VB>;
     constexpr int U = unroll<VB>();
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)(blockIdx.x / segs) * kTokWarps + (threadIdx.x >> 5);
+    const uint32_t at = blockIdx.x % segs * span + lane;  // this lane's first access in the row
+    const int left = (int)min((int64_t)span - lane, H / C::N - at);  // the segment's end from there
     ptx::griddep_wait();
-    if (item >= M * segs) return;
-    const int64_t t = item / segs;
-    const int64_t c0 = (item % segs) * (32 * U) + lane;  // this lane's first access in the row
-    const int64_t n = H / C::N;
+    if (t >= M) return;
     typename C::V v[U];
     bool loaded = false;
-    const auto* src = reinterpret_cast<const typename C::V*>(x + t * H);
+    const auto* src = reinterpret_cast<const typename C::V*>(x + t * H) + at;
     for (int j0 = 0; j0 < k; j0 += 32) {
         uint32_t place;
         uint32_t todo = places(scatter, t, k, j0, P, lane, &place);
         if (todo && !loaded) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c0 + 32 * u < n) v[u] = src[c0 + 32 * u];
+                if (32 * u < left) v[u] = src[32 * u];
             loaded = true;
         }
         for (; todo; todo &= todo - 1) {
             const uint32_t p = __shfl_sync(0xffffffffu, place, __ffs(todo) - 1);
-            auto* dst = reinterpret_cast<typename C::V*>(sorted + (int64_t)p * H);
+            auto* dst = reinterpret_cast<typename C::V*>(sorted + (int64_t)p * H) + at;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c0 + 32 * u < n) dst[c0 + 32 * u] = v[u];
+                if (32 * u < left) dst[32 * u] = v[u];
         }
     }
 }
 
 // One warp per (token, segment): the weighted sum of the token's rows, R of
 // them in flight at a time (without weights there is no residual either).
-// Narrow accesses are bound by the latency of a warp's two dependent reads,
-// places and rows: without weights, ten blocks an SM hide more of it (6 x 8191
-// fp32 rows of 1031, an eighth of the experts here: 16.1 us, 20.0 with six).
+// Bound by the latency of a warp's two dependent reads, places and rows, where
+// accesses are narrow: as many blocks an SM as the sums leave registers for.
+// (6 x 8191 fp32 rows of 1031, an eighth of the experts here: 10.3 us with nine,
+// 10.5 with eight; with ten, whose registers spill, 11.9.  6 x 4096 bf16 rows of
+// 1028, all experts: 10.4 with eight, 19.6 with ten.)
+constexpr int sum_blocks(int VB, bool weighted) {
+    return VB >= 16 ? 6 : VB >= 8 ? (weighted ? 5 : 8) : weighted ? 8 : 9;
+}
+
 template <typename T, int VB, bool WEIGHTED>
-__global__ void __launch_bounds__(kTokThreads, VB < 16 && !WEIGHTED ? 10 : 6)
+__global__ void __launch_bounds__(kTokThreads, sum_blocks(VB, WEIGHTED))
     combine_kernel(const T* y, int64_t M, int64_t H, const int32_t* __restrict__ scatter, int k, uint32_t P,
-                   const float* __restrict__ weights, const T* residual, T* out, int segs) {
+                   const float* __restrict__ weights, const T* residual, T* out, uint32_t segs, uint32_t span) {
     using C = Chunk<T, VB>;
-    constexpr int U = unroll<VB>() / 2, R = VB >= 16 ? 4 : 2;
+    constexpr int U = sum_unroll<VB>(), R = VB >= 16 ? 4 : 2;
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)(blockIdx.x / segs) * kTokWarps + (threadIdx.x >> 5);
+    const uint32_t at = blockIdx.x % segs * span + lane;  // this lane's first access in the row
+    const int left = (int)min((int64_t)span - lane, H / C::N - at);  // the segment's end from there
     ptx::griddep_wait();
-    if (item >= M * segs) return;
-    const int64_t t = item / segs;
-    const int64_t c0 = (item % segs) * (32 * U) + lane;
-    const int64_t n = H / C::N;
+    if (t >= M) return;
     float acc[U][C::N];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -126,10 +143,10 @@ __global__ void __launch_bounds__(kTokThreads, VB < 16 && !WEIGHTED ? 10 : 6)
         for (int i = 0; i < C::N; ++i) acc[u][i] = 0.0f;
     C r[U];
     if (WEIGHTED && residual != nullptr) {
-        const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H);
+        const auto* res = reinterpret_cast<const typename C::V*>(residual + t * H) + at;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + 32 * u < n) r[u].v = res[c0 + 32 * u];
+            if (32 * u < left) r[u].v = res[32 * u];
     }
     for (int j0 = 0; j0 < k; j0 += 32) {
         uint32_t place;
@@ -146,17 +163,17 @@ __global__ void __launch_bounds__(kTokThreads, VB < 16 && !WEIGHTED ? 10 : 6)
                 todo &= todo - 1;
                 const uint32_t p = __shfl_sync(0xffffffffu, place, j);
                 w[q] = WEIGHTED ? __shfl_sync(0xffffffffu, weight, j) : 1.0f;
-                const auto* src = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H);
+                const auto* src = reinterpret_cast<const typename C::V*>(y + (int64_t)p * H) + at;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (c0 + 32 * u < n) c[q][u].v = src[c0 + 32 * u];
+                    if (32 * u < left) c[q][u].v = src[32 * u];
             }
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 if (q >= rows) break;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (c0 + 32 * u < n)
+                    if (32 * u < left)
 #pragma unroll
                         for (int i = 0; i < C::N; ++i)
                             acc[u][i] = WEIGHTED ? fmaf(w[q], to_f32(c[q][u].t[i]), acc[u][i])
@@ -164,15 +181,15 @@ __global__ void __launch_bounds__(kTokThreads, VB < 16 && !WEIGHTED ? 10 : 6)
             }
         }
     }
-    auto* dst = reinterpret_cast<typename C::V*>(out + t * H);
+    auto* dst = reinterpret_cast<typename C::V*>(out + t * H) + at;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (c0 + 32 * u >= n) continue;
+        if (32 * u >= left) continue;
         C c;
 #pragma unroll
         for (int i = 0; i < C::N; ++i)
             c.t[i] = from_f32<T>(WEIGHTED && residual != nullptr ? acc[u][i] + to_f32(r[u].t[i]) : acc[u][i]);
-        dst[c0 + 32 * u] = c.v;
+        dst[32 * u] = c.v;
     }
 }
 
@@ -303,22 +320,20 @@ int check(const TokArgs& a, int dtype, std::initializer_list<const void*> rows,
 
 template <typename T, int VB>
 int run_gather(const TokArgs& a, const void* x, void* sorted) {
-    const int64_t n = a.H / (VB / (int)sizeof(T)), per = 32 * unroll<VB>();
-    const int segs = (int)((n + per - 1) / per);
-    const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
+    const Split s(a.H / (VB / (int)sizeof(T)), unroll<VB>());
+    const int64_t blocks = (a.M + kTokWarps - 1) / kTokWarps * s.segs;
     if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_gather_tokens: M*H needs too many blocks");
     return launch(gather_kernel<T, VB>, blocks, kTokThreads, a.who, a.stream, (const T*)x, a.M, a.H, a.scatter, a.k,
-                  (uint32_t)(a.M * a.k), (T*)sorted, segs);
+                  (uint32_t)(a.M * a.k), (T*)sorted, s.segs, s.span);
 }
 
 template <typename T, int VB, bool WEIGHTED>
 int run_combine(const TokArgs& a, const void* y, const float* w, const void* residual, void* out) {
-    const int64_t n = a.H / (VB / (int)sizeof(T)), per = 32 * (unroll<VB>() / 2);
-    const int segs = (int)((n + per - 1) / per);
-    const int64_t blocks = (a.M * segs + kTokWarps - 1) / kTokWarps;
+    const Split s(a.H / (VB / (int)sizeof(T)), sum_unroll<VB>());
+    const int64_t blocks = (a.M + kTokWarps - 1) / kTokWarps * s.segs;
     if (blocks >= (1ll << 31)) return set_error(MOE_ERR_UNSUPPORTED, "moe_combine_tokens: M*H needs too many blocks");
     return launch(combine_kernel<T, VB, WEIGHTED>, blocks, kTokThreads, a.who, a.stream, (const T*)y, a.M, a.H,
-                  a.scatter, a.k, (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, segs);
+                  a.scatter, a.k, (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, s.segs, s.span);
 }
 
 // A warp per pair from this many pairs on, a block per pair below.
