@@ -1239,8 +1239,8 @@ int stages_of(size_t room, int stage_bytes) {
 // leave room for more stages, which a product that waits for its weights
 // needs), but no more than lets the tiles reach every pair of SMs: a call of
 // few tiles takes as long as one of them.  (2-slot batch of 3373 tokens, one
-// expert here, 200 x 232 with every part of the epilogue: 9.4 us with tiles of
-// 32, 15.2 with tiles of 256.)
+// expert here, 200 x 232 with every part of the epilogue: 7.4 us with tiles of
+// 32, 13.4 with tiles of 256.)
 void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
@@ -1248,9 +1248,10 @@ void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     // Where even tiles of 32 leave most SMs idle, 2 or 4 pairs share a tile's
     // reduction: a tile's time is then its weight's rows through one pair's
     // L2 ports (46 bytes a cycle and SM).  One token, 2 of 8 experts, 1024 by
-    // 2 x 512: 7.5 us with four pairs, 8.1 with one; 16 rows of 20 experts,
-    // 1888 by 248: 10.7 and 12.9.  Only where all clusters run at once, so that
-    // each has at most one tile, whose sums need no second buffer.
+    // 2 x 512: 6.7 us with four pairs, 7.3 with one; 16 rows of 20 experts,
+    // 1888 by 248: 8.3 and 10.0; one row, 7168 by 256: 10.4 and 24.2.  Only where
+    // all clusters run at once, so that each has at most one tile, whose sums need
+    // no second buffer.
     a.split = 1;
     const int64_t most = (a.P / a.tn_max + (a.E < a.P ? a.E : a.P)) * a.tiles_f, blocks_k = (a.red + kBK - 1) / kBK;
     if (a.tn_max == 32 && most <= fit2)
