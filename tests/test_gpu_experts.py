@@ -104,6 +104,27 @@ def test_token_rows_at_every_alignment():
             ref.within(moe.combine_tokens(out, scatter, w, residual=x), ref.combine(out, scatter, w, x, k))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [64, 257, 288, 289, 385, 577, 768, 1154, 2308, 2881, 20011])
+def test_rows_of_many_widths(H, dtype):
+    """Widths around whole segments of every access size."""
+    M, k, E = 43, 5, 16
+    g = gen(H)
+    w, _, _, scatter = routing(M, k, E, g)
+    x, r, dout = randn(g, M, H, dtype=dtype), randn(g, M, H, dtype=dtype), randn(g, M, H, dtype=dtype)
+    xs = moe.gather_tokens(x, scatter, k)
+    assert torch.equal(xs[scatter.long()], x.repeat_interleave(k, 0))
+    y = randn(g, M * k, H, dtype=dtype)
+    ref.within(moe.combine_tokens(y, scatter, w, residual=r), ref.combine(y, scatter, w, r, k))
+    ref.within(moe.gather_tokens_backward(y, scatter, k), ref.combine(y, scatter, None, None, k))
+    dy, dw = moe.combine_tokens_backward(dout, y, scatter, w)
+    rows, _ = ref.rows_of(y, scatter, k)
+    dot = rows * dout.to(D)[:, None, :]
+    ref.within(dw, (dot.sum(2), (H + 8) * ref.U24 * dot.abs().sum(2)))
+    v = dout.to(D).repeat_interleave(k, 0) * w.reshape(-1, 1).to(D)
+    ref.within(dy[scatter.long()], (v, (ref.half_step(dtype) + ref.U24) * v.abs()))
+
+
 def test_token_offsets_pass_32_bits():
     """Row offsets beyond 2^32 bytes and 2^31 elements."""
     M, k, E, H = 40000, 8, 8, 7168
