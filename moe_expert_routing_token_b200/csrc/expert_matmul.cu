@@ -491,23 +491,34 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, const uint8_t* sums, in
     ptx::tmem_st_frag32(taddr, acc);
 }
 
+// A warp's part of the residual or the preactivations, 32 tokens of 32 lanes
+// from tok0 on: on its way while the chunk before is worked on.
+template <int MODE>
+struct Extra {
+    static constexpr int WIDTH = MODE == kFwdGated ? 32 : 64;  // bytes of one part per token
+    Rows<WIDTH> in0, in1;
+    __device__ __forceinline__ void load(const RowArgs& a, const Tile& t, int tok0, int quarter, int lane) {
+        if (a.extra == nullptr) return;
+        const int col0 = first_column<MODE>(t, quarter), valid = t.valid - tok0;
+        const int64_t ld = MODE == kGradGated ? 2 * (int64_t)a.N : a.N;
+        const bf16* p = a.extra + ((int64_t)t.row0 + tok0) * ld + col0;
+        in0.load(p, ld, valid, a.N - col0, lane);
+        if constexpr (MODE == kGradGated) in1.load(p + a.N, ld, valid, a.N - col0, lane);
+    }
+};
+
 // One warp's 32 lanes x 32 tokens of the accumulator at taddr.
 template <int MODE>
-__device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, const Bias<MODE>& bias, uint32_t taddr,
-                                               int tok0, int quarter, uint8_t* stage, int lane) {
-    constexpr int WIDTH = MODE == kFwdGated ? 32 : 64;       // bytes of one output part per token
+__device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, const Bias<MODE>& bias,
+                                               Extra<MODE>& extra, uint32_t taddr, int tok0, int quarter,
+                                               uint8_t* stage, int lane) {
     const int valid = t.valid - tok0;                        // tokens of this chunk (may exceed 32)
     const int col0 = first_column<MODE>(t, quarter);
     const int cols = a.N - col0;                             // columns left (may be <= 0)
     const int64_t row0 = (int64_t)t.row0 + tok0;
     const uint32_t sst = ptx::smem_u32(stage);
 
-    Rows<WIDTH> in0, in1;
     const int64_t ld_in = MODE == kGradGated ? 2 * (int64_t)a.N : a.N;
-    if (a.extra != nullptr) {
-        in0.load(a.extra + row0 * ld_in + col0, ld_in, valid, cols, lane);
-        if constexpr (MODE == kGradGated) in1.load(a.extra + row0 * ld_in + a.N + col0, ld_in, valid, cols, lane);
-    }
     float acc[2][4][4];
     ptx::tmem_ld_frag32(taddr, acc);
     const int groups = valid >= 32 ? 4 : (valid + 7) / 8;    // token groups of 8 in use
@@ -535,7 +546,8 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
         }
         uint32_t r[4][4];
         if (a.extra != nullptr) {
-            in0.stage(stage, lane);
+            extra.in0.stage(stage, lane);
+            extra.load(a, t, tok0 + 64, quarter, lane);
             __syncwarp();
             get32(sst, r, lane);
             __syncwarp();
@@ -582,7 +594,8 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
         }
         uint32_t r[4][2];
         if (a.extra != nullptr) {
-            in0.stage(stage, lane);
+            extra.in0.stage(stage, lane);
+            extra.load(a, t, tok0 + 64, quarter, lane);
             __syncwarp();
             get16(sst, r, lane);
             __syncwarp();
@@ -603,16 +616,17 @@ __device__ __forceinline__ void epilogue_chunk(const RowArgs& a, const Tile& t, 
     } else {
         uint32_t w[4][4] = {}, g[4][4], u[4][4] = {};
         if (a.extra != nullptr) {
-            in0.stage(stage, lane);
+            extra.in0.stage(stage, lane);
             __syncwarp();
             get32(sst, g, lane);
             __syncwarp();
             if constexpr (MODE == kGradGated) {
-                in1.stage(stage, lane);
+                extra.in1.stage(stage, lane);
                 __syncwarp();
                 get32(sst, u, lane);
                 __syncwarp();
             }
+            extra.load(a, t, tok0 + 64, quarter, lane);
         }
         if (a.extra == nullptr) {
 #pragma unroll
@@ -829,6 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             Bias<MODE> bias;
             bias.load(a, t, quarter, lane);
             prefetch_extra<MODE>(a, t, quarter, half, lane);
+            Extra<MODE> extra;
+            if (slice == 0) extra.load(a, t, half * 32, quarter, lane);
             if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs + blocks_k * kStageNs)) {
                 if (lane == 0) give_up(abort_flag);
                 *abort_flag = 1;
@@ -853,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (*abort_flag) break;
             }
             for (int tok0 = half * 32; tok0 < t.valid && slice == 0; tok0 += 64)
-                epilogue_chunk<MODE>(a, t, bias, base + tok0, tok0, quarter, stage, lane);
+                epilogue_chunk<MODE>(a, t, bias, extra, base + tok0, tok0, quarter, stage, lane);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), lead));
