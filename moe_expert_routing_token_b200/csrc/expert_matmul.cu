@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *abort_flag = 1;
             }
             __syncwarp();
-            if (*abort_flag) break;
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
             ptx::tc_fence_after();
             const uint32_t base = tmem + acc.s * kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
             if (a.split > 1 && half == 0) {
@@ -844,15 +844,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (slice > 0) {
                     send_sums(base, ptx::smem_u32(sums) + (slice - 1) * kSumBytes, ptx::smem_u32(&c->joined), rank,
                               quarter, lane);
-                } else if (ptx::mbar_wait_cluster(&c->joined, 0, kWaitNs + blocks_k * kStageNs)) {
-                    __syncwarp();
+                } else if (__all_sync(0xffffffffu, ptx::mbar_wait_cluster(&c->joined, 0,
+                                                                          kWaitNs + blocks_k * kStageNs))) {
                     add_sums(base, sums, a.split - 1, quarter, lane);
                 } else {
                     if (lane == 0) give_up(abort_flag);
                     *abort_flag = 1;
                 }
                 __syncwarp();
-                if (*abort_flag) break;
+                if (__any_sync(0xffffffffu, *abort_flag)) break;
             }
             for (int tok0 = half * 32; tok0 < t.valid && slice == 0; tok0 += 64)
                 epilogue_chunk<MODE>(a, t, bias, extra, base + tok0, tok0, quarter, stage, lane);
@@ -1027,7 +1027,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (left == 0) continue;
             if (runs_over(left)) {
                 const uint32_t bit = r.bar >> 3;
-                if (!ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs + before * kStageNs)) {
+                if (!__all_sync(0xffffffffu,
+                                ptx::bar_wait<false>(tail + r.bar, uses >> bit & 1, kWaitNs + before * kStageNs))) {
                     if (lane == 0) give_up(abort_flag);
                     break;
                 }
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *abort_flag = 1;
                 }
                 __syncwarp();
-                if (*abort_flag) break;
+                if (__any_sync(0xffffffffu, *abort_flag)) break;
                 ptx::tc_fence_after();
             }
             const uint32_t base =
