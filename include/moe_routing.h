@@ -535,8 +535,18 @@ typedef enum {
  *     grad_logits = sum_j grad_weights_j * dw_j / dx
  *   grad_weights   device, fp32 (M, k)
  *   gating_output  device, (M, E) of `dtype`: the logits that were routed
- *   topk_ids       device, int32 (M, k): the routing call's ids.  Ids outside
- *                  [0, E) (a shared-expert slot) are left out of every sum
+ *   topk_ids       device, int32 (M, k): the routing call's ids, as it wrote
+ *                  them (moe_sort_topk_by_id may have reordered them, with the
+ *                  weights).  Ids outside [0, E) are left out of every sum:
+ *                  the result is then the gradient of weights that were made
+ *                  without those slots
+ * Behind moe_fill_shared_expert_slot, which overwrites the last slot of a
+ * finished result: topk_ids are the ids from BEFORE the fill (a renormalised
+ * weight was divided by a sum that holds the overwritten expert's score), and
+ * grad_weights are taken back through the fill: with a factor, the last slot's
+ * weight was (sum of the others) / factor, so
+ *     grad_j += grad_last / factor  (j < k - 1),   grad_last = 0
+ * and without one the last slot kept its weight and keeps its gradient.
  *   scoring        MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
  *   softcap        finite, 0 = none; only with MOE_SCORE_SOFTMAX
  *   grad_logits    device, (M, E) of `dtype` out (written whole)

@@ -139,6 +139,20 @@ def topk_backward(grad_weights: torch.Tensor, gating_output: torch.Tensor, topk_
     choice of experts held fixed: (M, E) of the logits' dtype
     (moe_topk_backward).  ``scoring``: "softmax" (``topk_softmax``,
     ``grouped_topk``) or "sigmoid" (``biased_grouped_topk``, fused routers);
-    the other arguments as in the routing call."""
+    the other arguments as in the routing call.
+
+    ``topk_ids`` are the ids that the routing call wrote.  Where
+    ``fill_shared_expert_slot`` has overwritten the last slot (in place: keep
+    the ids from before), the weights' gradient dw goes back through the fill
+    first::
+
+        routed = ids.clone()
+        moe.fill_shared_expert_slot(w, ids, E, num_shared, pick, factor)
+        # ... the layer, forward and backward, with w and ids: dw
+        if factor is not None:
+            dw[:, :-1] += dw[:, -1:] / factor
+            dw[:, -1] = 0
+        dlogits = moe.topk_backward(dw, logits, routed, scoring, renormalize, rsf)
+    """
     return _native.topk_backward(grad_weights, gating_output, topk_ids, _named(SCORINGS, scoring, "scoring"),
                                  renormalize, routed_scaling_factor, softcap, out)

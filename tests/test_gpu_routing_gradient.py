@@ -1,0 +1,137 @@
+"""The routing gradient (moe_topk_backward) where a caller meets it: behind each
+routing call, behind a shared-expert slot, at saturated softcaps and at logits far
+below zero (GPU only)."""
+import inspect
+import re
+import textwrap
+
+import pytest
+import torch
+
+import moe_expert_routing_token_b200 as moe
+from tests import expert_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32, I32, D = torch.bfloat16, torch.float32, torch.int32, torch.float64
+U24 = ref.U24
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(g, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, generator=g, device=DEV) * scale).to(dtype)
+
+
+def definition(x, ids, g, scoring, renorm, cap, mag=None):
+    """(value, bound) in 64 bits of the gradient of sum_j g_j w_j with respect to
+    the logits x, for weights without a scaling factor.  ``mag``: magnitudes that
+    g was summed from, where it is a sum itself.
+
+    The bound follows the formula term by term, each with its sign taken off.  A
+    score, or the chosen ones' shares of their sum, is off by its exponent's
+    argument (one rounding of it, and of the capped logits by 4 units of cap:
+    tanhf and the products around it), expf (2 units in the last place) and a sum
+    of positive terms with a division, fewer than 64 + E / 32 roundings.  At most
+    three such factors meet in a term.  The cap's slope is 1 / cosh(t)^2 at
+    t = x / cap, rounded: 2 |t| units, and 16 for an exponential, its products
+    and a division."""
+    x = x.to(D)
+    ids, g = ids.long(), g.to(D)
+    mag = g.abs() if mag is None else mag.to(D)
+    t = x / cap if cap else torch.zeros_like(x)
+    z = cap * torch.tanh(t) if cap else x
+    slope = 1 / torch.cosh(t) ** 2
+    zj = z.gather(1, ids)
+    if scoring == "softmax" and not renorm:
+        p, spread = torch.softmax(z, 1), z.amax(1, keepdim=True) - z.amin(1, keepdim=True)
+        v, every = p.gather(1, ids), p
+    elif scoring == "softmax":
+        v, spread = torch.softmax(zj, 1), zj.amax(1, keepdim=True) - zj.amin(1, keepdim=True)
+    else:
+        log_p = torch.nn.functional.logsigmoid(zj)
+        q = torch.special.expit(-zj)
+        v = torch.softmax(log_p, 1) if renorm else log_p.exp()
+        spread = zj.amax(1, keepdim=True) - zj.amin(1, keepdim=True) if renorm else torch.zeros_like(zj[:, :1])
+    mean = (g * v).sum(1, keepdim=True)
+    lump = (mag * v).sum(1, keepdim=True)
+    value, size = torch.zeros_like(x), torch.zeros_like(x)
+    if scoring == "softmax" and not renorm:
+        value = -every * mean
+        size = every * lump
+        value.scatter_add_(1, ids, v * g)
+        size.scatter_add_(1, ids, v * mag)
+    elif scoring == "softmax":
+        value.scatter_add_(1, ids, v * (g - mean))
+        size.scatter_add_(1, ids, v * (mag + lump))
+    elif renorm:
+        value.scatter_add_(1, ids, v * (g - mean) * q)
+        size.scatter_add_(1, ids, v * (mag + lump) * q)
+    else:
+        value.scatter_add_(1, ids, v * g * q)
+        size.scatter_add_(1, ids, v * mag * q)
+    eps = (64 + x.shape[1] / 32 + 2 * spread + 8 * abs(cap)) * U24
+    return value * slope, (3 * eps + (2 * t.abs() + 16) * U24) * size * slope
+
+
+def check(got, value, bound):
+    """To the rounding of got's type, and 2^-120 where fp32 leaves its normal range."""
+    ref.within(got, (value, bound + ref.half_step(got.dtype) * (value.abs() + bound) + 2.0 ** -120))
+
+
+def route(M, k, E, dtype, seed, scale=2.0):
+    g = gen(seed)
+    x = randn(g, M, E, dtype=dtype, scale=scale)
+    ids = torch.rand(M, E, generator=g, device=DEV).argsort(1)[:, :k].to(I32).contiguous()
+    return x, ids, randn(g, M, k)
+
+
+# ---------------------------------------------------------------- behind the calls that make weights
+
+def shown(after):
+    """The indented example of topk_backward's documentation that follows ``after``."""
+    doc = inspect.getdoc(moe.topk_backward)
+    assert after in doc
+    lines = doc[doc.index(after):].split("::\n", 1)[1].strip("\n").split("\n")
+    n = next((i for i, line in enumerate(lines) if line and not line.startswith("    ")), len(lines))
+    return textwrap.dedent("\n".join(lines[:n]))
+
+
+@pytest.mark.parametrize("factor", [None, 2.5])
+@pytest.mark.parametrize("scoring,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False),
+                                            ("sigmoid", True)])
+@pytest.mark.parametrize("k", [1, 2, 6])
+def test_behind_a_shared_expert_slot(k, scoring, renorm, factor):
+    """The documented lines, run as they stand, give the gradient of the weights
+    that the layer used: the routing's, its last slot overwritten with the sum of
+    the others."""
+    M, E, rsf = 70, 160, 2.5
+    x, _, dw = route(M, k, E, F32, 3)
+    if scoring == "softmax":
+        w, ids = moe.grouped_topk(x, k, renorm, 8, 3, rsf)
+    else:
+        w, ids = moe.biased_grouped_topk(x, randn(gen(4), E, scale=0.05), k, renorm, 8, 4, rsf)
+    before, given = ids.clone(), dw.clone()
+    names = dict(moe=moe, w=w, ids=ids, logits=x, dw=dw, E=E, num_shared=2, factor=factor, scoring=scoring,
+                 renormalize=renorm, rsf=rsf, pick=torch.randint(0, 2, (M,), generator=gen(5), device=DEV, dtype=I32))
+    exec(shown("fill_shared_expert_slot"), names)
+    assert bool((ids[:, -1] >= E).all()) and torch.equal(ids[:, :-1], before[:, :-1])
+    # as a function of the logits: every slot's gradient reaches the slots its weight was made of
+    g, mag = given.to(D), given.to(D).abs()
+    if factor is not None:
+        g, mag = [torch.cat([a[:, :-1] + a[:, -1:] / factor, torch.zeros_like(a[:, -1:])], 1) for a in (g, mag)]
+    check(names["dlogits"], *definition(x, before, rsf * g, scoring, renorm, 0.0, rsf * mag))
+    # and by differences of the filled weights along a direction
+    h, d = 1e-4, torch.randn(M, E, generator=gen(6), device=DEV, dtype=D)
+
+    def value(logits):
+        v = ref.routed(logits, before, scoring, renorm, rsf, 0.0)
+        if factor is not None:
+            v = torch.cat([v[:, :-1], v[:, :-1].sum(1, keepdim=True) / factor], 1)
+        return (v * given.to(D)).sum(1)
+
+    want = (value(x.to(D) + h * d) - value(x.to(D) - h * d)) / (2 * h)
+    size = (names["dlogits"].to(D) * d).abs().sum(1) + rsf * given.to(D).abs().sum(1)
+    assert bool(((names["dlogits"].to(D) * d).sum(1) - want).abs().le(2e-5 * size).all())
