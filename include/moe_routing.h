@@ -522,8 +522,10 @@ MOE_API int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, c
                                           float* grad_bias, void* stream);
 
 typedef enum {
-    MOE_SCORE_SOFTMAX = 0, /* moe_topk_softmax, moe_grouped_topk(_softcap)    */
-    MOE_SCORE_SIGMOID = 1  /* moe_biased_grouped_topk(_aiter), fused routers  */
+    MOE_SCORE_SOFTMAX = 0, /* moe_topk_softmax, moe_grouped_topk(_softcap),
+                              moe_fused_router_top1                           */
+    MOE_SCORE_SIGMOID = 1  /* moe_biased_grouped_topk(_aiter),
+                              moe_fused_router_topk(_noalloc)                 */
 } moe_scoring_t;
 
 /*
@@ -534,7 +536,10 @@ typedef enum {
  *     w_j = routed_scaling_factor * p_{id_j} [/ sum_l p_{id_l} if renormalize]
  *     grad_logits = sum_j grad_weights_j * dw_j / dx
  *   grad_weights   device, fp32 (M, k)
- *   gating_output  device, (M, E) of `dtype`: the logits that were routed
+ *   gating_output  device, (M, E) of `dtype`: the logits that were routed (the
+ *                  fused routers' logits_out; moe_fused_router_top1's weight
+ *                  goes with renormalize 0, routed_scaling_factor 1 and its
+ *                  softcap)
  *   topk_ids       device, int32 (M, k): the routing call's ids, as it wrote
  *                  them (moe_sort_topk_by_id may have reordered them, with the
  *                  weights).  Ids outside [0, E) are left out of every sum:

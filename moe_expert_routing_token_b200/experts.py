@@ -137,9 +137,11 @@ def topk_backward(grad_weights: torch.Tensor, gating_output: torch.Tensor, topk_
                   out=None) -> torch.Tensor:
     """Gradient of a routing call's weights with respect to its logits, the
     choice of experts held fixed: (M, E) of the logits' dtype
-    (moe_topk_backward).  ``scoring``: "softmax" (``topk_softmax``,
-    ``grouped_topk``) or "sigmoid" (``biased_grouped_topk``, fused routers);
-    the other arguments as in the routing call.
+    (moe_topk_backward).  ``scoring``: "softmax" for ``topk_softmax``,
+    ``grouped_topk`` and ``fused_router_top1``, "sigmoid" for
+    ``biased_grouped_topk`` and ``fused_router_topk``; the other arguments as
+    in the routing call (``fused_router_top1``: ``renormalize`` False and its
+    ``softcap``; the fused routers' logits: ``return_logits``).
 
     ``topk_ids`` are the ids that the routing call wrote.  Where
     ``fill_shared_expert_slot`` has overwritten the last slot (in place: keep

@@ -135,3 +135,54 @@ def test_behind_a_shared_expert_slot(k, scoring, renorm, factor):
     want = (value(x.to(D) + h * d) - value(x.to(D) - h * d)) / (2 * h)
     size = (names["dlogits"].to(D) * d).abs().sum(1) + rsf * given.to(D).abs().sum(1)
     assert bool(((names["dlogits"].to(D) * d).sum(1) - want).abs().le(2e-5 * size).all())
+
+
+def softmax_weights(x, ids):
+    return torch.softmax(x, 1).gather(1, ids.long())
+
+
+def sigmoid_weights(x, ids):
+    p = torch.special.expit(x.gather(1, ids.long()))
+    return p / p.sum(1, keepdim=True)
+
+
+def top1_weight(x, ids):
+    z = 30.0 * torch.tanh(x / 30.0)
+    return 1 / torch.exp(z - z.gather(1, ids.long())).sum(1, keepdim=True)
+
+
+# routing call -> (its result on hidden rows, renormalize, softcap, its weights' definition)
+CALLS = {
+    "topk_softmax": (lambda h, W, x: (*moe.topk_softmax(x, 6, False), x), False, 0.0, softmax_weights),
+    "grouped_topk": (lambda h, W, x: (*moe.grouped_topk(x, 6, False, 8, 3), x), False, 0.0, softmax_weights),
+    "biased_grouped_topk": (lambda h, W, x: (*moe.biased_grouped_topk(x, None, 6, True, 8, 4), x), True, 0.0,
+                            sigmoid_weights),
+    "fused_router_topk": (lambda h, W, x: moe.fused_router_topk(h, W, None, 6, True, 8, 4, weight_layout="ek",
+                                                                return_logits=True), True, 0.0, sigmoid_weights),
+    "fused_router_top1": (lambda h, W, x: moe.fused_router_top1(h, W, softcap=30.0, return_logits=True), False, 30.0,
+                          top1_weight),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_scoring_documented_for_each_routing_call(name):
+    """With the scoring that the documentation names for a routing call,
+    topk_backward is the gradient of the weights that call returns."""
+    doc = " ".join(inspect.getdoc(moe.topk_backward).split())
+    named = {call: scoring for scoring, calls in re.findall(r'"(softmax|sigmoid)" for ((?:``\w+``(?:, | and )?)+)', doc)
+             for call in re.findall(r"``(\w+)``", calls)}
+    assert set(named) == set(CALLS)
+    call, renorm, cap, weights = CALLS[name]
+    g = gen(7)
+    h, W = randn(g, 200, 512, dtype=BF), randn(g, 256, 512, dtype=BF, scale=0.1)
+    w, ids, x = call(h, W, h.float() @ W.float().T)
+    xd = x.to(D).requires_grad_()
+    v = weights(xd, ids)
+    # a weight is a score of the routing kernels' own, to a part in 10^5
+    assert bool((w.to(D) - v).abs().le(1e-5 * v).all())
+    dw = randn(g, *w.shape)
+    (want,) = torch.autograd.grad((v * dw.to(D)).sum(), xd)
+    _, bound = definition(x, ids, dw, named[name], renorm, cap)
+    # 2^-48: the 64-bit derivative's own roundings where terms cancel
+    check(moe.topk_backward(dw, x, ids, named[name], renorm, softcap=cap), want,
+          bound + 2.0 ** -48 * dw.to(D).abs().sum(1, keepdim=True))
