@@ -555,6 +555,9 @@ typedef enum {
  *   scoring        MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
  *   softcap        finite, 0 = none; only with MOE_SCORE_SOFTMAX
  *   grad_logits    device, (M, E) of `dtype` out (written whole)
+ * Logits may be -inf here (masked experts): they get no gradient, and a row
+ * whose scores are all 0 gets zeros.  Finite logits have a finite gradient
+ * however far below zero they all lie.
  *   E <= 1024, 1 <= k <= 32, M * k below 2^31
  */
 MOE_API int moe_topk_backward(const float* grad_weights, const void* gating_output, int dtype,

@@ -6,8 +6,13 @@
 //   softmax, renorm    v_j = p_j / sum_l p_l is the softmax of the chosen z
 //                      alone: dz_j = v_j (g_j - sum_l g_l v_l), others 0
 //   sigmoid            dz_j = g_j p_j (1 - p_j)
-//   sigmoid, renorm    S = sum_l p_l: dz_j = (g_j - sum_l g_l p_l / S) / S * p_j (1 - p_j)
+//   sigmoid, renorm    v_j = p_j / sum_l p_l: dz_j = v_j (g_j - sum_l g_l v_l) (1 - p_j)
 //   softcap            dx = dz (1 - tanh(x / softcap)^2)
+//
+// Shares v_j come from scores scaled by exp(-m), m the largest chosen logit (of the
+// sigmoid's: where it is negative): sums of scores that fp32 cannot hold, as
+// sigmoids from about -87 on, never appear.  A scaled sum is 0 only where all its
+// logits are -inf; such a row gets zeros.
 //
 // Lane j of a group of L lanes (8, 16 or 32, as k needs) holds slot j of a row.
 // The row of the gradient is filled first, with zeros or, for the softmax
@@ -71,6 +76,9 @@ __device__ __forceinline__ float cap_slope(float x, float c) {
     return 1.0f - h * h;
 }
 
+// p / sum, 0 where nothing was summed (a NaN stays one).
+__device__ __forceinline__ float share(float p, float sum) { return sum != 0.0f ? p / sum : 0.0f; }
+
 // Sum over the slots of this group that share this lane's expert, and whether
 // this lane is the first of them.
 template <int L>
@@ -115,20 +123,21 @@ __global__ void __launch_bounds__(kGradWarps * 32) chosen_kernel(GradArgs a, int
     if (a.scoring == MOE_SCORE_SOFTMAX) {
         const float z = cap(raw, a.softcap);
         const float m = group_max<L>(mine ? z : -INFINITY);
-        float p = mine ? expf(z - m) : 0.0f;
-        const float s = group_sum<L>(p);
-        p = mine ? p / s : 0.0f;
+        float p = mine ? expf(z - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+        p = share(p, group_sum<L>(p));
         const float mean = group_sum<L>(g * p);
         v = p * (g - mean) * cap_slope(raw, a.softcap);
     } else {
-        const float p = mine ? 1.0f / (1.0f + expf(-raw)) : 0.0f;
         const float q = mine ? 1.0f / (1.0f + expf(raw)) : 0.0f;  // 1 - p without cancellation
-        v = g * p * q;
+        float p = mine ? 1.0f / (1.0f + expf(-raw)) : 0.0f, mean = 0.0f;
         if (a.renorm) {
-            const float s = group_sum<L>(p);
-            const float mean = group_sum<L>(g * p);
-            v = mine ? (g - mean / s) / s * p * q : 0.0f;
+            const float m = fminf(group_max<L>(mine ? raw : -INFINITY), 0.0f);
+            // all of them negative: p exp(-m) = exp(raw - m) q
+            if (mine && !(raw > 0.0f)) p = expf(raw - (m == -INFINITY ? 0.0f : m)) * q;
+            p = share(p, group_sum<L>(p));
+            mean = group_sum<L>(g * p);
         }
+        v = p * (g - mean) * q;
     }
     bool first;
     const float sum = joint<L>(v, id, mine, a.k, &first);
@@ -175,6 +184,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int 
         }
     }
     top = group_max<32>(top);
+    if (top == -INFINITY) top = 0.0f;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
@@ -186,8 +196,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) dense_kernel(GradArgs a, int 
         }
     }
     const float total = group_sum<32>(s);
-    const float p = mine ? expf(cap(raw, a.softcap) - top) / total : 0.0f;
-    const float rest = group_sum<32>(g * p), rest_total = rest / total;
+    const float p = mine ? share(expf(cap(raw, a.softcap) - top), total) : 0.0f;
+    const float rest = group_sum<32>(g * p), rest_total = share(rest, total);
     bool first;
     const float sum = joint<32>(g * p, id, mine, a.k, &first);
 #pragma unroll

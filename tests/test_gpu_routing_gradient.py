@@ -186,3 +186,51 @@ def test_scoring_documented_for_each_routing_call(name):
     # 2^-48: the 64-bit derivative's own roundings where terms cancel
     check(moe.topk_backward(dw, x, ids, named[name], renorm, softcap=cap), want,
           bound + 2.0 ** -48 * dw.to(D).abs().sum(1, keepdim=True))
+
+
+# ---------------------------------------------------------------- the ends of the logits' range
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("centre", [-80.0, -87.5, -88.5, -90.0, -104.0, -200.0, -1e30])
+@pytest.mark.parametrize("scoring,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True),
+                                            ("softmax", False)])
+@pytest.mark.parametrize("k", [1, 4, 12, 32])
+def test_logits_far_below_zero(k, scoring, renorm, centre, dtype):
+    """Rows whose sigmoids are below fp32's normal range, or vanish: the chosen
+    experts' shares of their sum, and with them the gradient, are those of any
+    other row."""
+    x, ids, dw = route(50, k, 64, dtype, 13)
+    x = (x.to(D) + centre).to(dtype)
+    got = moe.topk_backward(dw, x, ids, scoring, renorm)
+    check(got, *definition(x, ids, dw, scoring, renorm, 0.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("E", [64, 37, 1024])
+@pytest.mark.parametrize("scoring,renorm,cap", [("sigmoid", True, 0.0), ("sigmoid", False, 0.0), ("softmax", True, 0.0),
+                                                ("softmax", False, 0.0), ("softmax", True, 30.0),
+                                                ("softmax", False, 30.0)])
+def test_masked_logits(scoring, renorm, cap, E, dtype):
+    """Logits of -inf (masked experts) have no gradient and take no part in the
+    others'; a row of nothing else gets zeros.  A NaN stays in its row."""
+    k = 6
+    x, ids, dw = route(40, k, E, dtype, 17)
+    low = float("-inf")
+    x[0] = low                                      # a masked token
+    x[1].scatter_(0, ids[1].long(), low)            # nothing chosen is left
+    x[2, int(ids[2, 0])] = low                      # one of the chosen
+    x[3] = low
+    x[3, int(ids[3, 2])] = -1.5                     # all but one of them
+    x[4].masked_fill_(torch.rand(E, generator=gen(18), device=DEV) < 0.5, low)
+    x[5, int(ids[5, 1])] = float("nan")
+    got = moe.topk_backward(dw, x, ids, scoring, renorm, softcap=cap)
+    # a finite logit that far down has the same scores and slopes, to 2^-280
+    value, bound = definition(torch.where(x == low, -1e4 if cap else -200.0, x.to(D)), ids, dw, scoring, renorm, cap)
+    gone = (x == low).all(1) | ((x.gather(1, ids.long()) == low).all(1) if renorm or scoring == "sigmoid" else False)
+    value[gone], bound[gone] = 0.0, 0.0
+    value[x == low] = 0.0
+    plain = [r for r in range(40) if r != 5]
+    check(got[plain], value[plain], bound[plain])
+    assert bool(got[5].isnan().any())
+    if cap:  # a capped -inf is a score like others, with no slope
+        assert bool((got[plain][x[plain] == low] == 0).all())
