@@ -7,7 +7,7 @@
 //                      alone: dz_j = v_j (g_j - sum_l g_l v_l), others 0
 //   sigmoid            dz_j = g_j p_j (1 - p_j)
 //   sigmoid, renorm    v_j = p_j / sum_l p_l: dz_j = v_j (g_j - sum_l g_l v_l) (1 - p_j)
-//   softcap            dx = dz (1 - tanh(x / softcap)^2)
+//   softcap            dx = dz / cosh(x / softcap)^2
 //
 // Shares v_j come from scores scaled by exp(-m), m the largest chosen logit (of the
 // sigmoid's: where it is negative): sums of scores that fp32 cannot hold, as
@@ -69,11 +69,12 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 __device__ __forceinline__ float cap(float x, float c) { return c != 0.0f ? c * tanhf(x / c) : x; }
-// d cap / d x
+// d cap / d x = 1 / cosh(x / c)^2, with e = exp(-2 |x / c|).  (1 - tanh^2 has 6% of
+// error left at 8 caps and is 0 from 9 on.)
 __device__ __forceinline__ float cap_slope(float x, float c) {
     if (c == 0.0f) return 1.0f;
-    const float h = tanhf(x / c);
-    return 1.0f - h * h;
+    const float e = expf(-2.0f * fabsf(x / c));
+    return 4.0f * e / ((1.0f + e) * (1.0f + e));
 }
 
 // p / sum, 0 where nothing was summed (a NaN stays one).

@@ -234,3 +234,16 @@ def test_masked_logits(scoring, renorm, cap, E, dtype):
     assert bool(got[5].isnan().any())
     if cap:  # a capped -inf is a score like others, with no slope
         assert bool((got[plain][x[plain] == low] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("cap", [5.0, 30.0, -30.0])
+@pytest.mark.parametrize("k,E", [(1, 8), (8, 256), (20, 37)])
+def test_softcap_slope_keeps_its_precision(k, E, cap, renorm, dtype):
+    """Logits up to 25 caps out, where the slope 1 / cosh(t)^2 is down to 1e-21: a
+    relative bound, slope and all."""
+    x, ids, dw = route(60, k, E, dtype, 11, scale=8 * abs(cap))
+    x = x.clamp(-25 * abs(cap), 25 * abs(cap))
+    got = moe.topk_backward(dw, x, ids, "softmax", renorm, softcap=cap)
+    check(got, *definition(x, ids, dw, "softmax", renorm, cap))
