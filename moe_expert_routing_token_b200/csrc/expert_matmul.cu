@@ -40,7 +40,10 @@
 // tiles: one tile's latency.
 //
 // Every wait is bounded; a wait that runs out is counted
-// (moe_watchdog_trips) and ends the block's work.
+// (moe_watchdog_trips) and ends the block's work.  An accumulator whose
+// products are not all in is never handed to an epilogue, of either CTA (the
+// other one's flag is not set, only its own wait runs out): such a tile is not
+// stored and, of a split reduction, not sent on.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::umma_commit_pair(empty + r.bar, ctas);
                     r = next;
                 }
-                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), ctas);
+                if (ok) ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), ctas);
             }
         }
     } else if (warp >= 4) {
@@ -1010,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::umma_commit_pair(empty + r.bar, 3);
                     r = next;
                 }
-                ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), 3);
+                if (ok) ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), 3);
                 acc.step(2);
             }
         }
