@@ -40,3 +40,83 @@ def test_weight_gradients_error_in_the_mean(M, k, H, dtype):
     want = torch.stack([(y[scatter.view(M, k)[:, j].long()].to(D) * dout.to(D)).sum(1) for j in range(k)], 1)
     off = float((dw.to(D) - want).norm() / want.norm())
     assert off <= 0.425 * U24 * math.sqrt(28), off / U24
+
+
+def values_of_bf16(low, high):
+    """Every bf16 value between, in rows of 64 (filled up with zeros)."""
+    v = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(BF).float()
+    v = v[(v >= low) & (v <= high) & (v.abs() >= 2.0 ** -20)]
+    v = torch.nn.functional.pad(v, (0, -len(v) % 64)).view(-1, 64)
+    return v.to(BF).to(DEV)
+
+
+def exact(z, act):
+    """f and f' in 64 bits, with the normal distribution from erfc: from erf, as
+    1 + erf, it cancels in the tail."""
+    if act == "silu":
+        p, q = torch.special.expit(z), torch.special.expit(-z)
+        return z * p, p + z * p * q
+    normal = 0.5 * torch.special.erfc(-z / math.sqrt(2))
+    return z * normal, normal + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+
+
+def activation_bounds(z, act):
+    """Error of f and f' at an exact z, relative to their terms.
+
+    GELU: Phi(-|z|) = density * ratio; the density's exponent z^2 / 2 is rounded
+    twice, z^2 units of 2^-24; ex2 (4 units), the fitted ratio (12 units, 20 for
+    its Horner steps and the reciprocal) and products make 48.  f = max(z, 0) -
+    |z| Phi(-|z|) and f' = z phi + Phi join them with a rounding of the result;
+    Phi = 1 - Phi(-z) for z > 0 with one more of 1.
+    SiLU: p = 1 / (1 + exp(-z)); exp's argument is rounded by 2 |z| units, and
+    matters by 1 - p; ex2, sum and reciprocal make 12.  f = z p; f' = p + f (1 - p),
+    where 1 - p is off by p's error.
+    Exponentials and reciprocals below 2^-126 are 0."""
+    u = z.abs()
+    value, rate = exact(z, act)
+    if act == "gelu":
+        phi = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        tail = 0.5 * torch.special.erfc(u / math.sqrt(2))
+        e = z * z + 48
+        f = U24 * (e * u * tail + value.abs())
+        slope = U24 * (e * tail + e * u * phi + rate.abs() + (z > 0))
+    else:
+        p, q = torch.special.expit(z), torch.special.expit(-z)
+        e = U24 * p * (2 * u * q + 12)
+        f = u * e + U24 * u * p
+        slope = e + f * q + u * p * (e + U24 * (q + (z > 0))) + U24 * (rate.abs() + p * u * q)
+    end = (1 + u) * 2.0 ** -125
+    return f + end, slope + end
+
+
+@pytest.mark.parametrize("act,low,high", [("gelu", -14.5, 14.5), ("silu", -100.0, 100.0)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations_at_every_bf16_value(gated, act, low, high):
+    """An identity weight makes the preactivations exact: f and f' are held to
+    bounds relative to their own terms, down to where the tails leave fp32."""
+    z = values_of_bf16(low, high)
+    P = z.shape[0]
+    off = torch.tensor([0, P], dtype=I32, device=DEV)
+    one = torch.eye(64, device=DEV, dtype=BF)[None]
+    f, df = exact(z.to(D), act)
+    ef, edf = activation_bounds(z.to(D), act)
+    bf = ref.half_step(BF)
+    floor = 2.0 ** -133  # bf16's own spacing at the end of its range
+
+    def check(got, value, bound):
+        ref.within(got, (value, bound + bf * (value.abs() + bound) + floor))
+
+    if gated:  # the other factor is a bias of one
+        weight = torch.cat([one, torch.zeros_like(one)], 1).contiguous()
+        bias = torch.cat([torch.zeros(1, 64, device=DEV), torch.ones(1, 64, device=DEV)], 1)
+        check(moe.expert_matmul(z, weight, off, bias=bias, activation=act, gated=True), f, ef)
+    else:
+        check(moe.expert_matmul(z, one, off, activation=act), f, ef)
+    dy = torch.ones_like(z)
+    if gated:
+        both = torch.cat([z, torch.ones_like(z)], 1).contiguous()
+        got = moe.expert_matmul_grad_input(dy, one, off, preact=both, activation=act, gated=True)
+        check(got[:, :64], df, edf)
+        check(got[:, 64:], f, ef)
+    else:
+        check(moe.expert_matmul_grad_input(dy, one, off, preact=z, activation=act), df, edf)
