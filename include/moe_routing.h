@@ -513,9 +513,11 @@ MOE_API int moe_expert_matmul_grad_input(const void* grad_out, const void* weigh
  *   grad_weight  device, (E, N, K) of `dtype` out, 16-byte aligned
  *   grad_bias    device, fp32 (E, N) out, or NULL
  *   K, N, E      as moe_expert_matmul
- * The products' fp32 sums are the tensor cores', which cut rather than round:
- * an fp32 grad_weight is off by 2e-6 (2-norm, relative) for 2048 rows an
- * expert of random signs, 5e-7 for 512.
+ * The products' fp32 sums are the tensor cores', which cut rather than round,
+ * in parts of 2048 rows (16384 for a bf16 grad_weight) that are joined with
+ * rounded additions: an fp32 grad_weight is off by 5e-7 (2-norm, relative) for
+ * 512 rows an expert of random signs, by 2e-6 for 2048 and more (6e-6 where
+ * all terms are positive).
  */
 MOE_API int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int32_t* expert_offsets,
                                           int64_t P, int32_t K, int32_t N, int32_t E, int dtype, void* grad_weight,

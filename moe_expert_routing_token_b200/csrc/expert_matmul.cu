@@ -28,8 +28,9 @@
 // expert_weight_kernel (grad_weight).  A tile is 256 x 256 of one expert's
 // gradient, both operands MN-major with the reduction along tokens.  Where a
 // segment's last 64-row stage runs over its end, the next segment's rows are
-// zeroed in shared memory before the product.  The result leaves by tile
-// stores, which clip at the matrix's ends.
+// zeroed in shared memory before the product.  Long segments are summed in
+// parts, the later ones in the second accumulator and from there added onto the
+// first.  The result leaves by tile stores, which clip at the matrix's ends.
 //
 // What bounds them (B200): long reductions over many rows, a pair's two SMs
 // taking 64 bytes a cycle each from L2 (256 x 256 x 64 takes 516 cycles and
@@ -878,6 +879,20 @@ constexpr int kWStageBytes = kABytes + kWN / 2 * kBK * 2;
 __device__ __forceinline__ int steps_of(int left) { return left >= kBK ? kBK / 16 : (left + 15) / 16; }
 __device__ __forceinline__ bool runs_over(int left) { return left < kBK && left % 16 != 0; }
 
+// A segment's rows are summed in parts, whose sums are joined by rounded additions
+// (the epilogue adds a part onto the first one's accumulator): the tensor core cuts
+// its running sum to 24 bits at each step of 16 rows instead of rounding it, which
+// grows with the steps: relative, for terms of random signs, 2.1e-6 after 2048 rows,
+// 9.1e-6 after 8192, 1.5e-4 after 131072 (5.6e-6, 3.5e-5 and 8e-4 where all are
+// positive).  Parts as the result's type needs them: an addition holds the products
+// up for 0.85 us, 1600 cycles for 768 of TMEM traffic (fp32, 4 experts of 8192 rows,
+// 4096 by 4096: 898 us, 774 - 802 in one sum; bf16 has one addition to 16384 rows).
+template <typename T>
+__device__ __forceinline__ int part_end(int p0, int count) {
+    constexpr int kPart = sizeof(T) == 4 ? 2048 : 16384;
+    return count - p0 > kPart ? p0 + kPart : count;
+}
+
 // A warp's 32 rows x 128 bytes, staged in the 128-byte swizzle of its tile
 // store: lane r holds row r, whose 16-byte piece c lies at c ^ (r % 8).
 template <typename T>
@@ -970,7 +985,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0 && elect_one()) {
             const uint32_t idesc = ptx::idesc_bf16_m256(kWN, true, true);
             Stages r;
-            Ring acc;
+            int s = 0;               // the tile's accumulator: its first part's
+            uint32_t filled = 0;     // parity of each accumulator's uses
             // parity of each stage's uses, whole and cut (bit of its barrier's offset)
             uint32_t uses[2] = {0, 0};
             bool ok = true, ready = false;  // ready: the stage at r is known to be full
@@ -979,42 +995,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
                 const int count = seg.count(tile / per_e);
                 if (count == 0) continue;
-                if (!ptx::mbar_wait_cluster(&c->acc_empty[acc.s], acc.phase ^ 1, kWaitNs)) {
-                    give_up(abort_flag);
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d = tmem + acc.s * kAccCols;
-                for (int p = 0; p < count; p += kBK) {
-                    const uint32_t bit = r.bar >> 3;
-                    const bool over = runs_over(count - p);
-                    if (!ready) {
-                        ok = over ? ptx::bar_wait<true>(cut + r.bar, uses[1] >> bit & 1, kWaitNs)
-                                  : ptx::bar_wait<true>(full + r.bar, uses[0] >> bit & 1, kWaitNs);
-                        if (!ok) {
-                            give_up(abort_flag);
-                            break;
-                        }
+                for (int p0 = 0, end; p0 < count && ok; p0 = end) {
+                    end = part_end<T>(p0, count);
+                    const int a_s = p0 == 0 ? s : s ^ 1;
+                    if (!ptx::mbar_wait_cluster(&c->acc_empty[a_s], (filled >> a_s & 1) ^ 1, kWaitNs)) {
+                        give_up(abort_flag);
+                        ok = false;
+                        break;
                     }
-                    if (over) uses[1] ^= 1u << bit;
-                    else uses[0] ^= 1u << bit;
-                    Stages next = r;
-                    next.step(kWStageBytes, all);
-                    // look ahead within the segment
-                    ready = count - p > kBK && !runs_over(count - p - kBK) &&
-                            ptx::bar_try_cluster(full + next.bar, uses[0] >> (next.bar >> 3) & 1);
+                    filled ^= 1u << a_s;
                     ptx::tc_fence_after();
-                    const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
-                    const int steps = steps_of(count - p);
+                    const uint32_t d = tmem + a_s * kAccCols;
+                    for (int p = p0; p < end; p += kBK) {
+                        const uint32_t bit = r.bar >> 3;
+                        const bool over = runs_over(count - p);
+                        if (!ready) {
+                            ok = over ? ptx::bar_wait<true>(cut + r.bar, uses[1] >> bit & 1, kWaitNs)
+                                      : ptx::bar_wait<true>(full + r.bar, uses[0] >> bit & 1, kWaitNs);
+                            if (!ok) {
+                                give_up(abort_flag);
+                                break;
+                            }
+                        }
+                        if (over) uses[1] ^= 1u << bit;
+                        else uses[0] ^= 1u << bit;
+                        Stages next = r;
+                        next.step(kWStageBytes, all);
+                        // look ahead within the segment
+                        ready = count - p > kBK && !runs_over(count - p - kBK) &&
+                                ptx::bar_try_cluster(full + next.bar, uses[0] >> (next.bar >> 3) & 1);
+                        ptx::tc_fence_after();
+                        const uint64_t ad = ad0 + (r.at >> 4), bd = bd0 + (r.at >> 4);
+                        const int steps = steps_of(count - p);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        if (kk < steps)
-                            ptx::umma_bf16_pair(d, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), idesc, (p | kk) != 0);
-                    ptx::umma_commit_pair(empty + r.bar, 3);
-                    r = next;
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            if (kk < steps)
+                                ptx::umma_bf16_pair(d, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), idesc,
+                                                    p != p0 || kk != 0);
+                        ptx::umma_commit_pair(empty + r.bar, 3);
+                        r = next;
+                    }
+                    if (ok) ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[a_s]), 3);
                 }
-                if (ok) ptx::umma_commit_pair(ptx::smem_u32(&c->acc_full[acc.s]), 3);
-                acc.step(2);
+                s ^= 1;
             }
         }
     } else if (warp == 3) {
@@ -1052,24 +1075,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         const int ew = warp - 4, quarter = warp & 3, half = ew >> 2;
         uint8_t* stage = epi + ew * kWEpiBytes;
-        Ring acc;
+        int s = 0;
+        uint32_t seen = 0;  // parity of each accumulator's uses
         for (unsigned tile = pair; tile < tiles; tile += pairs) {
             const int e = tile / per_e;
             const unsigned in = tile - e * per_e;
             const int row = (in / a.tiles_k * 2 + rank) * kM + quarter * 32;
             const int k0 = in % a.tiles_k * kWN + half * (kWN / 2);
             const bool some = seg.count(e) > 0;
-            if (some) {
-                if (!ptx::mbar_wait(&c->acc_full[acc.s], acc.phase, kWaitNs + seg.count(e) / kBK * kStageNs)) {
+            const uint32_t lanes = tmem + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
+            const uint32_t base = lanes + s * kAccCols;
+            bool whole = true;
+            for (int p0 = 0, end, count = seg.count(e); p0 < count; p0 = end) {
+                end = part_end<T>(p0, count);
+                const int a_s = p0 == 0 ? s : s ^ 1;
+                if (!ptx::mbar_wait(&c->acc_full[a_s], seen >> a_s & 1, kWaitNs + (end - p0) / kBK * kStageNs)) {
                     if (lane == 0) give_up(abort_flag);
                     *abort_flag = 1;
                 }
                 __syncwarp();
-                if (__any_sync(0xffffffffu, *abort_flag)) break;
+                if (__any_sync(0xffffffffu, *abort_flag)) {
+                    whole = false;
+                    break;
+                }
+                seen ^= 1u << a_s;
                 ptx::tc_fence_after();
+                if (p0 == 0) continue;
+                ptx::tmem_add(base, lanes + a_s * kAccCols, kWN / 2);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[a_s]), 0));
             }
-            const uint32_t base =
-                tmem + acc.s * kAccCols + half * (kWN / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
+            if (!whole) break;
             constexpr int COLS = 128 / (int)sizeof(T);  // of one tile store
 #pragma unroll 1
             for (int j = 0; j < kWN / 2; j += COLS) {
@@ -1093,8 +1130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (some) {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[acc.s]), 0));
-                acc.step(2);
+                if (lane == 0) ptx::bar_arrive_remote(ptx::map_to_rank(ptx::smem_u32(&c->acc_empty[s]), 0));
+                s ^= 1;
             }
         }
         if (lane == 0) ptx::tma_store_wait();

@@ -158,6 +158,38 @@ __device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const float (&v)[
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 32 columns of this warp's 32 lanes back to TMEM, as tmem_ld32 loads them; to be
+// waited for (tcgen05.wait::st) before they are read.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// `cols` columns (a multiple of 32) of this warp's 32 lanes at `from` onto those at
+// `to`, rounded.
+__device__ __forceinline__ void tmem_add(uint32_t to, uint32_t from, int cols) {
+#pragma unroll 1
+    for (int j = 0; j < cols; j += 32) {
+        float a[32], b[32];
+        tmem_ld32(to + j, a);
+        tmem_ld32(from + j, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a[i] += b[i];
+        tmem_st32(to + j, a);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // Four 8x8 matrices of 16-bit values between registers (thread l holds row
 // l / 4, columns 2 (l % 4) + {0, 1}) and shared memory, transposed: the 16
 // bytes at the address that thread 8 m + i gives are column i of matrix m.

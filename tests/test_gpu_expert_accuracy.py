@@ -120,3 +120,40 @@ def test_activations_at_every_bf16_value(gated, act, low, high):
         check(got[:, 64:], f, ef)
     else:
         check(moe.expert_matmul_grad_input(dy, one, off, preact=z, activation=act), df, edf)
+
+
+LONG = [([5000], 264, 136), ([8192, 0, 2048, 2049, 4096], 256, 256), ([40000, 3, 17000], 72, 264), ([131077], 256, 64)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("counts,K,N", LONG)
+def test_weight_gradients_of_many_rows(counts, K, N, positive, dtype):
+    """The tensor core cuts its running sum at each step of 16 rows, by up to a unit
+    of 2^-23; a part of 2048 rows (16384 for bf16 results) is summed that way, parts
+    are joined with rounded additions.  So the error relative to the sum of the
+    terms' magnitudes does not grow with the rows beyond a part's steps and half a
+    unit per part.  For random signs, by the root mean square: a running sum of i of
+    n steps is sqrt(i / n) of the part's in the mean, 2/3 n units of 2^-23 in all at
+    the most."""
+    g = torch.Generator(device=DEV).manual_seed(sum(counts))
+    off = torch.tensor([0] + counts, device=DEV).cumsum(0).to(I32)
+    P, part = sum(counts), 2048 if dtype == F32 else 16384
+    dy, x = randn(g, P, N, dtype=BF), randn(g, P, K, dtype=BF)
+    if positive:
+        dy, x = dy.abs(), x.abs()
+    dw = moe.expert_matmul_grad_weight(dy, x, off, dtype=dtype)
+    for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        want, size = (torch.zeros(N, K, dtype=D, device=DEV) for _ in range(2))
+        for c in range(a, b, 32768):
+            d, r = dy[c:min(b, c + 32768)].to(D), x[c:min(b, c + 32768)].to(D)
+            want += d.T @ r
+            size += d.abs().T @ r.abs()
+        parts = -(-(b - a) // part)
+        bound = (ref.sum_bound(min(b - a, part)) + parts * U24) * size
+        ref.within(dw[e], (want, bound + ref.half_step(dtype) * (want.abs() + bound)))
+        if dtype == F32 and not positive and b > a:
+            mean = (2 / 3 * (min(b - a, part) / 16 + 16) * 2 + math.sqrt(parts)) * U24
+            assert float((dw[e].to(D) - want).norm() / want.norm()) <= mean
+    if len(counts) == 1:
+        assert torch.equal(moe.expert_matmul_grad_weight(dy, x, off, dtype=dtype), dw)
