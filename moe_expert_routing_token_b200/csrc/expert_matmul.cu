@@ -130,9 +130,11 @@ __device__ __forceinline__ float2 mills(float2 t) {
     return mul2(p, rcp_2(q));
 }
 
-// f(z) and, where asked for, f'(z) of two values.  The epilogue is bound by
-// issued instructions, hence two values an instruction wherever there is one
-// for it; the approximate exponential's and reciprocal's few units in the 24th
+// f(z) and, where asked for, f'(z) of two values.  Where the reduction is short the
+// epilogue's time is the call's (6335 rows, 176 by 4664: 41 us with GELU, 24
+// without an activation): two warps a scheduler, each a chain of dependent steps
+// (issue slots 42% busy, fixed latencies the most frequent stall), hence two
+// values an instruction wherever there is one for it; the approximate exponential's and reciprocal's few units in the 24th
 // bit vanish in the rounding to bf16.  A NaN stays one.
 template <int ACT, bool GRAD>
 __device__ __forceinline__ float2 activate(float2 z, float2* slope) {
@@ -954,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t part = ring_at + (warp == 0 ? 0 : kABytes);
             for (unsigned tile = pair; tile < tiles && ok; tile += pairs) {
                 const int e = tile / per_e;
-            const unsigned in = tile - e * per_e;
+                const unsigned in = tile - e * per_e;
                 const int c0 = warp == 0 ? (in / a.tiles_k * 2 + rank) * kM : in % a.tiles_k * kWN + rank * (kWN / 2);
                 const int count = seg.count(e), row0 = seg.begin[e];
                 for (int p = 0; p < count; p += kBK) {
@@ -1284,6 +1286,12 @@ int stages_of(size_t room, int stage_bytes) {
 // few tiles takes as long as one of them.  (2-slot batch of 3373 tokens, one
 // expert here, 200 x 232 with every part of the epilogue: 7.4 us with tiles of
 // 32, 13.4 with tiles of 256.)
+// The bounds on the mean, in us with tiles of 32 / 64 / 128 / 256 (uneven
+// segments, 0.75 to 1.25 of the mean; 160 experts, 1544 by 1024, and 64, 7168 by
+// 2048):  mean 16: 85 / 90 / 95 / 96, 277 / 272 / 273 / 272;  mean 32: 103 / 94 /
+// 99 / 103, 307 / 278 / 283 / 285;  mean 56: 150 / 108 / 102 / 109, 404 / 295 /
+// 291 / 304;  mean 128: 263 / 193 / 160 / 121, 714 / 509 / 409 / 339.  The rule is
+// within 8% of the best width for means of 4 to 300.
 void choose_tile(RowArgs& a, int pairs, int fit2, int fit4) {
     const int64_t mean = (a.P + a.E - 1) / a.E;
     a.tn_max = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 80 ? 128 : 256;
@@ -1503,7 +1511,7 @@ int moe_expert_matmul_grad_weight(const void* grad_out, const void* x, const int
     WeightArgs a = {expert_offsets, P, E, N, K, (unsigned)(N + 2 * kM - 1) / (2 * kM),
                     (unsigned)(K + kWN - 1) / kWN, 0, grad_bias != nullptr};
     const size_t fixed = fixed_bytes(E, kEpiWarps * kWEpiBytes);
-    a.stages = stages_of(kSmemMax - fixed, kWStageBytes);  // 6 up to 400 experts, else 5
+    a.stages = stages_of(kSmemMax - fixed, kWStageBytes);  // 6 up to 201 experts, else 5
     const size_t smem = fixed + (size_t)a.stages * kWStageBytes;
     const int64_t tiles = (int64_t)a.E * a.tiles_n * a.tiles_k;
     rc2 = check_tiles(who, tiles);

@@ -63,7 +63,9 @@ __device__ __forceinline__ uint32_t places(const int32_t* scatter, int64_t t, in
 }
 
 // Accesses a lane has in flight per row: 64 bytes, at most 12 accesses; for sums
-// half of that, at most 9.
+// half of that, at most 9: an odd width a little past a power of two takes no
+// more segments than the power (sums of 6 x 4096 fp32 rows of 515 / 1031 / 2051:
+// 12.6 / 22.0 / 39.8 us; with eight 13.8 / 22.4 / 40.0, with ten 12.7 / 22.4 / 39.7).
 template <int VB> constexpr int unroll() { return VB >= 16 ? 4 : VB >= 8 ? 8 : 12; }
 template <int VB> constexpr int sum_unroll() { return VB >= 16 ? 2 : VB >= 8 ? 4 : 9; }
 
@@ -117,9 +119,10 @@ __global__ void __launch_bounds__(kTokThreads)
 // them in flight at a time (without weights there is no residual either).
 // Bound by the latency of a warp's two dependent reads, places and rows, where
 // accesses are narrow: as many blocks an SM as the sums leave registers for.
-// (6 x 8191 fp32 rows of 1031, an eighth of the experts here: 10.3 us with nine,
-// 10.5 with eight; with ten, whose registers spill, 11.9.  6 x 4096 bf16 rows of
-// 1028, all experts: 10.4 with eight, 19.6 with ten.)
+// (From warm caches, 6 x 8191 fp32 rows of 1031, an eighth of the experts here:
+// 10.3 us with nine, 10.5 with eight; with ten, whose registers spill, 11.9.
+// 6 x 4096 bf16 rows of 1028, all experts: 10.4 with eight, 19.6 with ten.  From
+// HBM the first takes 14.9, the second 17.6.)
 constexpr int sum_blocks(int VB, bool weighted) {
     return VB >= 16 ? 6 : VB >= 8 ? (weighted ? 5 : 8) : weighted ? 8 : 9;
 }
@@ -197,8 +200,9 @@ __global__ void __launch_bounds__(kTokThreads, sum_blocks(VB, WEIGHTED))
 // row of grad_out comes from cache for all but its first slot.  The dot product
 // is summed in blocks, the U accesses of a round in two chains: 1.1e-7 off in the
 // mean for fp32 rows of 7168, where one chain over a lane's whole share was
-// 2.75e-7 (304 us for 4096 x 8 of them, both).  U accesses of either row in flight, as many as four blocks an SM have registers for
-// (4096 x 6 bf16 rows of 1028: 24.9 us, 33.8 with eight in 100 registers).
+// 2.75e-7 (304 us for 4096 x 8 of them, both).  U accesses of either row in
+// flight, as many as four blocks an SM have registers for (4096 x 6 bf16 rows of
+// 1028: 25.8 us; 33.8 with eight in 100 registers).
 template <typename T, int VB, int W>
 __global__ void __launch_bounds__(256, 4)
     combine_backward_kernel(const T* grad_out, const T* y, int64_t pairs, int64_t H,
@@ -345,7 +349,9 @@ int run_combine(const TokArgs& a, const void* y, const float* w, const void* res
                   a.scatter, a.k, (uint32_t)(a.M * a.k), w, (const T*)residual, (T*)out, s.segs, s.span);
 }
 
-// A warp per pair from this many pairs on, a block per pair below.
+// A warp per pair from this many pairs on, a block per pair below.  Rows of 7168
+// bf16, in us with a warp / a block: 10.5 / 8.5 for 1024 pairs, 13.9 / 14.7 for
+// 2048, 22.3 / 26.7 for 4096; of 512 bf16: 4.6 / 3.6, 4.4 / 8.2, 4.6 / 14.3.
 constexpr int64_t kWarpPairs = 4096;
 
 template <typename T, int VB>

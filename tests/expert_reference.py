@@ -43,8 +43,10 @@ def sum_bound(n):
     return (math.ceil(n / 16) + 16) * 2 * U24
 
 
-# |f'| <= 1.13 for both activations; expf, normcdff and a division are a few
-# units in the last place, and expf's argument carries one rounding of z.
+# |f'| <= 1.13 for both activations.  act_error is absolute: an approximate
+# exponential (its argument carries roundings of z) and reciprocal, and GELU's
+# fitted ratio, a few units of 2^-23 of the result's largest term.  It is wide far
+# into the tails; tests/test_gpu_expert_accuracy.py bounds those relative to them.
 SLOPE = 1.13
 
 
