@@ -348,7 +348,8 @@ MOE_API int moe_expert_permutation(const int32_t* topk_ids, const float* topk_we
  *   routed_scaling_factor   0 = "None": the last slot's weight is left as it
  *                  is; otherwise it becomes (sum of the row's other k-1
  *                  weights, fp32 in slot order) / routed_scaling_factor
- * The last slot's id becomes E + shared_pick[row].  k <= 32; M = 0 is a no-op.
+ * The last slot's id becomes E + shared_pick[row]; for a backward pass keep
+ * the ids from before (moe_topk_backward).  k <= 32; M = 0 is a no-op.
  */
 MOE_API int moe_fill_shared_expert_slot(float* topk_weights, int32_t* topk_ids, int64_t M, int32_t k, int32_t E,
                                         int32_t num_shared, const int32_t* shared_pick,

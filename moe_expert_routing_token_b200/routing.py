@@ -367,7 +367,8 @@ def fill_shared_expert_slot(topk_weights: torch.Tensor, topk_ids: torch.Tensor, 
                             num_shared: int, shared_pick: torch.Tensor, routed_scaling_factor=None):
     """In place: the last slot of each row -> shared expert num_experts +
     shared_pick[row]; its weight -> sum of the other weights /
-    routed_scaling_factor (unchanged when it is None)."""
+    routed_scaling_factor (unchanged when it is None).  For a backward pass
+    keep the ids from before (``topk_backward``)."""
     M, k = _result_pair(topk_weights, topk_ids)
     if not shared_pick.is_cuda or shared_pick.dtype != torch.int32 or shared_pick.numel() != M or \
             not shared_pick.is_contiguous():

@@ -188,6 +188,62 @@ def test_scoring_documented_for_each_routing_call(name):
           bound + 2.0 ** -48 * dw.to(D).abs().sum(1, keepdim=True))
 
 
+@pytest.mark.parametrize("factor,scoring", [(2.5, "sigmoid"), (None, "softmax")])
+def test_a_layer_with_a_shared_expert(factor, scoring):
+    """Route, fill the last slot, run the layer on E + 2 experts forward and backward,
+    the documented lines for the router: against autograd of all of it in 64 bits, to
+    six roundings to bf16 (half a step is 2^-8) by the norm."""
+    M, k, E, H, F, rsf = 90, 3, 8, 128, 64, 2.5
+    g = gen(31)
+    x, dout = randn(g, M, H, dtype=BF), randn(g, M, H, dtype=BF)
+    W1, W2 = randn(g, E + 2, 2 * F, H, dtype=BF, scale=H ** -0.5), randn(g, E + 2, H, F, dtype=BF, scale=F ** -0.5)
+    logits = randn(g, M, E)
+    w, ids = (moe.topk_softmax(logits, k, True) if scoring == "softmax"
+              else moe.biased_grouped_topk(logits, None, k, True, 1, 1, rsf))
+    rsf = 1.0 if scoring == "softmax" else rsf
+    before = ids.clone()
+    pick = torch.randint(0, 2, (M,), generator=g, device=DEV, dtype=I32)
+
+    example = shown("fill_shared_expert_slot").split("\n")
+    cut = next(i for i, line in enumerate(example) if line.startswith("#"))
+    names = dict(moe=moe, w=w, ids=ids, logits=logits, E=E, num_shared=2, factor=factor, pick=pick, scoring=scoring,
+                 renormalize=True, rsf=rsf)
+    exec("\n".join(example[:cut]), names)
+    _, offsets, _, scatter, _ = moe.expert_permutation(ids, E + 2)
+    xs = moe.gather_tokens(x, scatter, k)
+    h, z = moe.expert_matmul(xs, W1, offsets, activation="silu", gated=True, return_preact=True)
+    y = moe.expert_matmul(h, W2, offsets)
+    out = moe.combine_tokens(y, scatter, w, residual=x)
+    dy, names["dw"] = moe.combine_tokens_backward(dout, y, scatter, w)
+    exec("\n".join(example[cut:]), names)
+
+    leaf = logits.to(D).requires_grad_()
+    v = ref.routed(leaf, before, scoring, True, rsf, 0.0)
+    if factor is not None:
+        v = torch.cat([v[:, :-1], v[:, :-1].sum(1, keepdim=True) / factor], 1)
+    total, xd = x.to(D), x.to(D)
+    for j in range(k):
+        e = ids[:, j].long()
+        zz = torch.einsum("mh,mnh->mn", xd, W1.to(D)[e])
+        total = total + v[:, j:j + 1] * torch.einsum("mf,mhf->mh", ref.f(zz[:, :F], "silu") * zz[:, F:], W2.to(D)[e])
+    (want,) = torch.autograd.grad((total * dout.to(D)).sum(), leaf)
+    for got, exact in ((out, total.detach()), (names["dlogits"], want)):
+        assert float((got.to(D) - exact).norm() / exact.norm()) <= 6 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("scoring,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_of_a_result_in_ascending_ids(scoring, renorm):
+    """sort_topk_by_id moves weights and ids together; so does their gradient."""
+    M, k, E = 50, 6, 160
+    x, _, dw = route(M, k, E, F32, 23)
+    w, ids = (moe.topk_softmax(x, k, renorm) if scoring == "softmax"
+              else moe.biased_grouped_topk(x, None, k, renorm, 1, 1, 1.0))
+    moe.sort_topk_by_id(w, ids)
+    v = ref.routed(x.to(D), ids, scoring, renorm, 1.0, 0.0)
+    assert bool((w.to(D) - v).abs().le(1e-5 * v).all())
+    check(moe.topk_backward(dw, x, ids, scoring, renorm), *definition(x, ids, dw, scoring, renorm, 0.0))
+
+
 # ---------------------------------------------------------------- the ends of the logits' range
 
 @pytest.mark.parametrize("dtype", [BF, F32])
