@@ -402,8 +402,8 @@ MOE_API int moe_sort_topk_by_id(float* topk_weights, int32_t* topk_ids, int64_t 
  *     whose running sum is cut, not rounded, at each step of 16 terms: 2e-6
  *     relative after 2048 terms of random signs, 9e-6 after 8192, below a
  *     bf16 rounding up to some 10^6.  The weight gradient, whose reduction is
- *     the rows, sums in parts: see there.)  Results do not depend on timing: the same
- *     inputs give the same bits.
+ *     the rows, sums in parts: see there.)  Results do not depend on timing:
+ *     the same inputs give the same bits.
  *   - Outputs must not overlap inputs or one another.
  *   - M * k must be below 2^31 and P below 2^31 - 256, else
  *     MOE_ERR_UNSUPPORTED.  M == 0 or P == 0 is valid
